@@ -335,6 +335,167 @@ PN_API pn_status pn_eval_static(const float* params, size_t n_params, int D, int
  * on cuda_stream and the call synchronises it.  For accuracy tests. */
 PN_API pn_status pn_activation(int which, const float* x, float* y, long long n, void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * Sequence-layer operators: linear attention with a decay for each head, and
+ * what its queries and keys go through before it -- per-head norms and the
+ * rotation by position.  (Additions of this library; the paper has no
+ * counterpart.  The recurrence is linear with a matrix state, so its chunked
+ * form is exact in one pass, where pn_eval iterates.)
+ *
+ * Conventions of these entry points:
+ *  - They are asynchronous: the work is ordered on cuda_stream and the call
+ *    returns without waiting.  They allocate nothing on the device and can be
+ *    captured into a CUDA graph.  Device and pinned memory must stay alive
+ *    until the stream has run the work.
+ *  - Plans and handles hold host memory only and never change after creation:
+ *    one may serve any device, stream and thread, several at once.
+ *  - Rows of heads are pn_heads: element (b, t, h, j) is at
+ *    data[b batch_stride + t token_stride + h head_stride + j] (strides in
+ *    elements, >= 0, rows contiguous).  16-byte aligned data and strides that
+ *    are multiples of 16 bytes run fastest; any others are correct.  Outputs
+ *    must not overlap each other or, except where said, inputs.
+ *  - Workspaces are the caller's (16-byte aligned device memory of at least the
+ *    size that the query returns for the same shape); a call leaves nothing in
+ *    one for the next call.  Calls that may overlap need one each.
+ *  - Every array must be on one device; the work runs there whichever device is
+ *    current.  Errors leave their text in pn_last_error(NULL).
+ */
+typedef enum { PN_F32 = 0, PN_BF16 = 1, PN_F16 = 2 } pn_dtype;
+
+typedef struct {
+  void* data;               /* device */
+  long long batch_stride, token_stride, head_stride;
+} pn_heads;
+
+/* Rotary positions.  Pair i = 0 .. rot_dim/2 - 1 of a head vector at position p
+ * turns by the angle p f_i and is multiplied by m:
+ *   (a, b) -> m (a cos - b sin, b cos + a sin).
+ * The other dim - rot_dim elements pass through.  Angles are formed in 64-bit
+ * fixed point, modulo a turn: off by at most |p| 2^-61 radians, however far the
+ * position; sine and cosine are float32. */
+typedef struct pn_rotary_plan* pn_rotary;
+typedef enum {
+  PN_ROT_HALF = 0,        /* pair i: elements i and i + rot_dim/2 */
+  PN_ROT_INTERLEAVED = 1  /* pair i: elements 2i and 2i + 1 */
+} pn_rotary_layout;
+typedef enum {
+  PN_ROT_PLAIN = 0,   /* f_i = base^(-2i/rot_dim) */
+  PN_ROT_LINEAR = 1,  /* f_i / factor */
+  PN_ROT_NTK = 2,     /* base times factor^(rot_dim/(rot_dim - 2)) */
+  PN_ROT_YARN = 3     /* f_i (g + (1 - g) / factor), g = clamp((r - beta_slow) / (beta_fast -
+                         beta_slow), 0, 1), r = original_length f_i / 2 pi turns over the original
+                         context; m = 0.1 ln(factor) + 1 */
+} pn_rotary_scaling;
+typedef struct {
+  int rot_dim;              /* even, 2 .. 256 */
+  int layout;               /* pn_rotary_layout */
+  int scaling;              /* pn_rotary_scaling */
+  double base;              /* > 1 */
+  double factor;            /* >= 1; ignored by PN_ROT_PLAIN */
+  long long original_length;         /* PN_ROT_YARN */
+  double beta_fast, beta_slow;       /* PN_ROT_YARN */
+  double attention_scale;   /* m; 0: 1, or PN_ROT_YARN's */
+} pn_rotary_desc;
+
+PN_API pn_status pn_rotary_create(pn_rotary* out, const pn_rotary_desc* desc);
+PN_API void pn_rotary_destroy(pn_rotary r);
+
+/* Rotate queries and keys in one launch.
+ *   dtype      pn_dtype of q, k and the outputs
+ *   B, T       batch entries and tokens of each; Hq, Hk heads; dim even, <= 256
+ *   positions  device [B][T], any int64
+ *   inverse    1: by the opposite angles (times m): the gradient of inverse = 0
+ *   q_out, k_out  may be q and k themselves (the same data and strides) */
+PN_API pn_status pn_rotary_apply(pn_rotary r, int dtype, int B, int T, int Hq, int Hk, int dim,
+                                 const pn_heads* q, const pn_heads* k, const long long* positions,
+                                 int inverse, const pn_heads* q_out, const pn_heads* k_out,
+                                 void* cuda_stream);
+
+/* The norm of each head vector, then its rotation, in one pass:
+ *   y_j = x_j w_j / sqrt(mean(x^2) + eps),
+ * over all dim elements, in float32 with one rounding at the end.
+ *   r       may be NULL: no rotation (positions is then ignored)
+ *   wq, wk  device [dim], of type w_dtype: PN_F32 or dtype */
+PN_API pn_status pn_norm_rotary_apply(pn_rotary r, int dtype, int B, int T, int Hq, int Hk, int dim,
+                                      const pn_heads* q, const pn_heads* k, const long long* positions,
+                                      const void* wq, const void* wk, int w_dtype, float eps,
+                                      const pn_heads* q_out, const pn_heads* k_out, void* cuda_stream);
+
+/* Its gradient: from dq_out, dk_out (gradients of the outputs) and the inputs q, k of the forward
+ * call, dq and dk (may be dq_out and dk_out themselves) and the weights' gradients dwq, dwk
+ * (device float32 [dim], overwritten; summed in a fixed order, so a repeated call gives the same
+ * bits). */
+PN_API size_t pn_norm_rotary_workspace(int B, int T, int Hq, int Hk, int dim);
+PN_API pn_status pn_norm_rotary_backward(pn_rotary r, int dtype, int B, int T, int Hq, int Hk, int dim,
+                                         const pn_heads* dq_out, const pn_heads* dk_out,
+                                         const pn_heads* q, const pn_heads* k,
+                                         const long long* positions, const void* wq, const void* wk,
+                                         int w_dtype, float eps, const pn_heads* dq, const pn_heads* dk,
+                                         float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                                         void* cuda_stream);
+
+/* Linear attention with a decay for each head: for every sequence and query head h, with the key
+ * and value head h / (H / Hkv),
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T     (dk x dv, float32)
+ *   o_t = scale q_t S_t.
+ * q, k, v and o are of one type (PN_F32, PN_BF16, PN_F16); states are float32.  An infinite or NaN
+ * input makes outputs of its sequence and head undefined from up to 127 rows before it (whole chunks
+ * are multiplied at once); other sequences, padding rows and rows behind the last one never
+ * take part. */
+typedef struct pn_linattn_s* pn_linattn;
+
+/*   H, Hkv     query heads (<= 256), key and value heads (Hkv divides H)
+ *   dk, dv     multiples of 8, 8 .. 256
+ *   log_decay  host [H], finite and <= 0 (copied); fixed: no gradient is formed for it */
+PN_API pn_status pn_linattn_create(pn_linattn* out, int H, int Hkv, int dk, int dv, int dtype,
+                                   const float* log_decay, float scale);
+PN_API void pn_linattn_destroy(pn_linattn h);
+
+/* Prompts: all rows of n_seq sequences (n_seq * H <= 65535).
+ *   cu_seqlens  NULL: n_seq sequences of T rows each, at the batch strides.  Else device int32
+ *               [n_seq + 1], not decreasing: sequence s is rows cu_seqlens[s] .. cu_seqlens[s+1] - 1
+ *               of one buffer of T rows (batch strides ignored).  Offsets outside 0 .. T are
+ *               clamped to it.  Sequences may be empty; rows before the first and behind the last
+ *               one are neither read nor written.
+ *   max_len     the longest sequence (ragged; 0 = not known): a hint that only the work's split
+ *               goes by, any value >= 0 is correct.  Workspace query and call take the same one.
+ *   initial_state  device [n_seq][H][dk][dv] or NULL (zero)
+ *   final_state    the same shape, or NULL; may be initial_state.  An empty sequence's final state
+ *               is its initial one.  Both 16-byte aligned. */
+PN_API size_t pn_linattn_workspace(pn_linattn h, int backward, int n_seq, long long T, int ragged,
+                                   long long max_len);
+PN_API pn_status pn_linattn_forward(pn_linattn h, int n_seq, long long T, const int* cu_seqlens,
+                                    long long max_len, const pn_heads* q, const pn_heads* k,
+                                    const pn_heads* v, const float* initial_state, const pn_heads* o,
+                                    float* final_state, void* workspace, size_t workspace_bytes,
+                                    void* cuda_stream);
+
+/* Gradients of pn_linattn_forward.  d_o and d_final_state (NULL = zero) are the gradients of its
+ * outputs; dq, dk, dv and d_initial_state (may be NULL, or d_final_state itself) receive those of its
+ * inputs.  dk and dv sum over the query heads that share them, in a fixed order.  Rows of no sequence
+ * are left as they are. */
+PN_API pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const int* cu_seqlens,
+                                     long long max_len, const pn_heads* d_o, const pn_heads* q,
+                                     const pn_heads* k, const pn_heads* v, const float* initial_state,
+                                     const float* d_final_state, const pn_heads* dq, const pn_heads* dk,
+                                     const pn_heads* dv, float* d_initial_state, void* workspace,
+                                     size_t workspace_bytes, void* cuda_stream);
+
+/* One token of each of `rows` (<= 65535) sequences, in one launch: the states are updated in place.
+ *   q, k, v, o  row b at batch_stride (token_stride ignored)
+ *   states      device [n_slots][H][dk][dv], 16-byte aligned
+ *   slots       device int64 [rows], or NULL (row b is slot b).  A row whose slot is outside
+ *               0 .. n_slots - 1 is padding: its output and every state are left as they are.  So
+ *               is a row that names the slot of an earlier row: a slot takes one token per call.
+ *   r, wq, wk   NULL, or what the queries and keys go through first, in the same pass: the norm
+ *               with weights wq, wk [dk] (both or neither) and the rotation r by positions
+ *               (device int64 [rows]); as pn_norm_rotary_apply but without its last rounding. */
+PN_API pn_status pn_linattn_step(pn_linattn h, int rows, const pn_heads* q, const pn_heads* k,
+                                 const pn_heads* v, const pn_heads* o, float* states, long long n_slots,
+                                 const long long* slots, pn_rotary r, const long long* positions,
+                                 const void* wq, const void* wk, int w_dtype, float eps,
+                                 void* cuda_stream);
+
 /* Shape queries (for the binding); each returns -1 for a NULL handle.
  * which = 0..4: D, d_in, T, B, cell.  which = 5 + mode: 1 when that mode's
  * iteration kernel loops over the iterations on the device (one launch per

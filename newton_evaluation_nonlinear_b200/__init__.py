@@ -8,6 +8,9 @@ iteration a fused cell + Jacobian evaluation and a chunked parallel scan
 (§2.1), all in sm_100a CUDA kernels behind the C ABI of ``include/pn.h``.
 
 This package is the ctypes binding of that library; see :mod:`._binding`.
+:mod:`._layers` holds the sequence-layer operators: linear attention with a
+decay for each head (:class:`LinearAttention`) and the norms and rotary positions
+of its queries and keys (:class:`Rotary`).
 """
 from ._binding import (MODES, PN_CELL_EULER_TANH, PN_CELL_GRU, PN_CELL_TANH_RNN, PN_ERR_CUDA,  # noqa: F401
                        PN_ERR_INVALID, PN_ERR_NOMEM, PN_ERR_NONFINITE, PN_ERR_TIMEOUT, PN_JACOBI,
@@ -20,5 +23,8 @@ from ._binding import (MODES, PN_CELL_EULER_TANH, PN_CELL_GRU, PN_CELL_TANH_RNN,
                        pn_get_mode_history, pn_get_stats, pn_last_error, pn_reset_stats, pn_set_adaptive,
                        pn_set_damping, pn_set_option, pn_set_storage, pn_set_stream,
                        pn_time_iterations, pn_version)
+from ._binding import (PN_BF16, PN_F16, PN_F32, PN_ROT_HALF, PN_ROT_INTERLEAVED, PN_ROT_LINEAR,  # noqa: F401
+                       PN_ROT_NTK, PN_ROT_PLAIN, PN_ROT_YARN, pn_heads, pn_rotary_desc)
+from ._layers import LinearAttention, Rotary  # noqa: F401
 
 __version__ = "0.1.0"

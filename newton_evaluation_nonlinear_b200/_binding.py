@@ -27,6 +27,9 @@ PN_OPT_RUN_LENGTH = 5
 PN_OPT_SMALL_SOLVE = 6
 PN_STORE_F32, PN_STORE_BF16, PN_STORE_F16 = 0, 1, 2
 PN_MAX_D_DIAG, PN_MAX_D_NEWTON = 256, 64
+PN_F32, PN_BF16, PN_F16 = 0, 1, 2
+PN_ROT_HALF, PN_ROT_INTERLEAVED = 0, 1
+PN_ROT_PLAIN, PN_ROT_LINEAR, PN_ROT_NTK, PN_ROT_YARN = 0, 1, 2, 3
 
 STATUS_NAMES = {PN_OK: "PN_OK", PN_NOT_CONVERGED: "PN_NOT_CONVERGED", PN_ERR_INVALID: "PN_ERR_INVALID",
                 PN_ERR_NOMEM: "PN_ERR_NOMEM", PN_ERR_CUDA: "PN_ERR_CUDA",
@@ -35,12 +38,28 @@ MODES = {"jacobi": PN_JACOBI, "picard": PN_PICARD, "quasi": PN_QUASI, "newton": 
 
 # Every symbol include/pn.h declares, with (restype, argtypes).
 _c_int, _c_float, _vp, _c_ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
+_c_size = ctypes.c_size_t
 
 
 class pn_stats(ctypes.Structure):
     _fields_ = [("iteration_launches", ctypes.c_longlong), ("iteration_ns", ctypes.c_longlong),
                 ("evals", ctypes.c_longlong)]
 
+
+class pn_heads(ctypes.Structure):
+    """Rows of heads: element (b, t, h, j) at data[b batch_stride + t token_stride + h head_stride + j]."""
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class pn_rotary_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("original_length", ctypes.c_longlong),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attention_scale", ctypes.c_double)]
+
+
+_heads = ctypes.POINTER(pn_heads)
 
 SIGNATURES = {
     "pn_create": (_c_int, [ctypes.POINTER(_vp), _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
@@ -66,6 +85,24 @@ SIGNATURES = {
     "pn_activation": (_c_int, [_c_int, _vp, _vp, _c_ll, _vp]),
     "pn_eval_static": (_c_int, [_vp, ctypes.c_size_t, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _c_int,
                                 _c_float, _vp, ctypes.POINTER(_c_int), ctypes.POINTER(_c_float), _vp]),
+    "pn_rotary_create": (_c_int, [ctypes.POINTER(_vp), ctypes.POINTER(pn_rotary_desc)]),
+    "pn_rotary_destroy": (None, [_vp]),
+    "pn_rotary_apply": (_c_int, [_vp] + [_c_int] * 6 + [_heads, _heads, _vp, _c_int, _heads, _heads, _vp]),
+    "pn_norm_rotary_apply": (_c_int, [_vp] + [_c_int] * 6 + [_heads, _heads, _vp, _vp, _vp, _c_int, _c_float,
+                                                             _heads, _heads, _vp]),
+    "pn_norm_rotary_workspace": (_c_size, [_c_int] * 5),
+    "pn_norm_rotary_backward": (_c_int, [_vp] + [_c_int] * 6 + [_heads] * 4 + [_vp, _vp, _vp, _c_int, _c_float,
+                                                                               _heads, _heads, _vp, _vp, _vp,
+                                                                               _c_size, _vp]),
+    "pn_linattn_create": (_c_int, [ctypes.POINTER(_vp), _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_float]),
+    "pn_linattn_destroy": (None, [_vp]),
+    "pn_linattn_workspace": (_c_size, [_vp, _c_int, _c_int, _c_ll, _c_int, _c_ll]),
+    "pn_linattn_forward": (_c_int, [_vp, _c_int, _c_ll, _vp, _c_ll, _heads, _heads, _heads, _vp, _heads, _vp, _vp,
+                                    _c_size, _vp]),
+    "pn_linattn_backward": (_c_int, [_vp, _c_int, _c_ll, _vp, _c_ll] + [_heads] * 4 + [_vp, _vp] + [_heads] * 3
+                            + [_vp, _vp, _c_size, _vp]),
+    "pn_linattn_step": (_c_int, [_vp, _c_int] + [_heads] * 4 + [_vp, _c_ll, _vp, _vp, _vp, _vp, _vp, _c_int,
+                                                               _c_float, _vp]),
     "pn_last_error": (ctypes.c_char_p, [_vp]),
     "pn_destroy": (None, [_vp]),
     "pn_version": (ctypes.c_char_p, []),

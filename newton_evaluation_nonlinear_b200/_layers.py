@@ -1,0 +1,344 @@
+"""torch-facing wrappers of the sequence-layer operators (include/pn.h): argument checks and marshalling only.
+
+:class:`Rotary` rotates queries and keys by position, with or without the norm of each head vector before it;
+:class:`LinearAttention` is the recurrence S_t = exp(g_h) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t, over whole prompts
+and for single tokens.  Gradients are explicit calls (``apply_backward``, ``norm_backward``, ``backward``); results
+carry no autograd graph.
+
+Tensors are [tokens, heads, dim] or [batch, tokens, heads, dim], CUDA, of one of the types float32, bfloat16 and
+float16, with contiguous rows and any other strides (slices of one projection's output go in as they are).  The work
+is asynchronous on torch's current stream of the tensors' device; the calls can be captured into a CUDA graph.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import numpy as np
+
+from ._binding import (PN_BF16, PN_F16, PN_F32, PN_OK, PN_ROT_HALF, PN_ROT_INTERLEAVED, PN_ROT_LINEAR, PN_ROT_NTK,
+                       PN_ROT_PLAIN, PN_ROT_YARN, PnError, lib, pn_heads, pn_last_error, pn_rotary_desc)
+
+_LAYOUTS = {"half": PN_ROT_HALF, "interleaved": PN_ROT_INTERLEAVED}
+_SCALINGS = {"none": PN_ROT_PLAIN, "linear": PN_ROT_LINEAR, "ntk": PN_ROT_NTK, "yarn": PN_ROT_YARN}
+_DTYPES = None
+
+
+def _dtypes():
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: PN_F32, torch.bfloat16: PN_BF16, torch.float16: PN_F16}
+    return _DTYPES
+
+
+def _dtype(name, t):
+    code = _dtypes().get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} is {t.dtype}: float32, bfloat16 or float16 is wanted")
+    return code
+
+
+def _ok(status: int) -> None:
+    if status != PN_OK:
+        raise PnError(status, pn_last_error(None))
+
+
+def _same(name, t, like):
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} is {t.dtype} on {t.device}; {like.dtype} on {like.device} is wanted")
+
+
+def _heads(name, t, like, lead=None, heads=None, dim=None):
+    """pn_heads of a [tokens, heads, dim] or [batch, tokens, heads, dim] tensor."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _same(name, t, like)
+    shape = t.shape
+    if (lead is not None and tuple(shape[:-2]) != tuple(lead)) or (heads is not None and shape[-2] != heads) \
+            or (dim is not None and shape[-1] != dim):
+        raise ValueError(f"{name} has shape {tuple(shape)}; {(*(lead or ('..',)), heads, dim)} is wanted")
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.dim() == 3:
+        return pn_heads(t.data_ptr(), 0, st[0], st[1])
+    return pn_heads(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _distinct(name, t):
+    """Outputs whose elements share memory (expanded tensors) are refused."""
+    for n, s in zip(t.shape, t.stride()):
+        if n > 1 and s == 0:
+            raise ValueError(f"{name} has overlapping elements")
+
+
+def _ints(name, t, shape, dtype, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _float32(name, t, shape, device):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _weights(wq, wk, dim, like):
+    """Pointers and type of a norm's weights: float32, or the queries' type."""
+    for name, w in (("wq", wq), ("wk", wk)):
+        if tuple(w.shape) != (dim,) or not w.is_contiguous() or w.device != like.device or w.dtype != wq.dtype:
+            raise ValueError(f"{name} must be a contiguous [{dim}] tensor on {like.device}, both weights of one type")
+    return wq.data_ptr(), wk.data_ptr(), _dtype("wq", wq)
+
+
+def _stream(device):
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _workspace(n, device):
+    """(tensor that keeps it, pointer) of n bytes of torch's own memory, used on the current stream."""
+    import torch
+    if not n:
+        return None, None
+    w = torch.empty(n, dtype=torch.uint8, device=device)
+    return w, w.data_ptr()
+
+
+class Rotary:
+    """The rotation of the first ``rot_dim`` elements of each head vector by its position.
+
+    layout    "half" (pair i: elements i and i + rot_dim/2) or "interleaved" (2i and 2i + 1)
+    scaling   "none"; "linear" (positions divided by ``factor``); "ntk" (the base stretched by ``factor``); "yarn"
+              (per frequency, by its turns over ``original_length``)
+    attention_scale   factor on the rotated elements; None: 1, or 0.1 ln(factor) + 1 for "yarn"
+
+    The plan holds no device memory; one object serves every device and stream.
+    """
+
+    def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 attention_scale: Optional[float] = None):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout {layout!r}: one of {sorted(_LAYOUTS)}")
+        if scaling not in _SCALINGS:
+            raise ValueError(f"scaling {scaling!r}: one of {sorted(_SCALINGS)}")
+        if attention_scale is not None and not attention_scale > 0:
+            raise ValueError("attention_scale must be > 0")
+        self.h = None
+        self.rot_dim = int(rot_dim)
+        desc = pn_rotary_desc(self.rot_dim, _LAYOUTS[layout], _SCALINGS[scaling], float(base), float(factor),
+                              int(original_length), float(beta_fast), float(beta_slow), float(attention_scale or 0.0))
+        h = ctypes.c_void_p()
+        _ok(lib.pn_rotary_create(ctypes.byref(h), ctypes.byref(desc)))
+        self.h = h.value
+
+    def __del__(self):
+        if getattr(self, "h", None):
+            lib.pn_rotary_destroy(self.h)
+            self.h = None
+
+    @staticmethod
+    def _shape(q, k):
+        hq = _heads("q", q, q)
+        hk = _heads("k", k, q, lead=q.shape[:-2], dim=q.shape[-1])
+        B, T = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
+        return hq, hk, (_dtype("q", q), B, T, q.shape[-2], k.shape[-2], q.shape[-1])
+
+    def _out(self, q, k, out):
+        import torch
+        if out is None:
+            out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        oq, ok = out
+        hq = _heads("out[0]", oq, q, q.shape[:-2], q.shape[-2], q.shape[-1])
+        hk = _heads("out[1]", ok, q, k.shape[:-2], k.shape[-2], k.shape[-1])
+        _distinct("out[0]", oq)
+        _distinct("out[1]", ok)
+        return out, hq, hk
+
+    def _rotate(self, q, k, positions, out, inverse):
+        import torch
+        hq, hk, shape = self._shape(q, k)
+        pos = _ints("positions", positions, q.shape[:-2], torch.int64, q.device)
+        out, oq, ok = self._out(q, k, out)
+        _ok(lib.pn_rotary_apply(self.h, *shape, hq, hk, pos, inverse, oq, ok, _stream(q.device)))
+        return out
+
+    def apply(self, q, k, positions, out=None):
+        """(q, k) rotated.  positions: int64, the shape of q without heads and dim.  ``out``: a pair of tensors, which may
+        be (q, k) themselves."""
+        return self._rotate(q, k, positions, out, 0)
+
+    def apply_backward(self, dq, dk, positions, out=None):
+        """Gradients of the inputs of :meth:`apply` from those of its outputs: the rotation by the opposite angles."""
+        return self._rotate(dq, dk, positions, out, 1)
+
+    def norm_apply(self, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
+        """x_j w_j / sqrt(mean(x^2) + eps) of each head vector, then the rotation, in one pass.  The weights are [dim],
+        float32 or of the queries' type."""
+        import torch
+        hq, hk, shape = self._shape(q, k)
+        pos = _ints("positions", positions, q.shape[:-2], torch.int64, q.device)
+        out, oq, ok = self._out(q, k, out)
+        _ok(lib.pn_norm_rotary_apply(self.h, *shape, hq, hk, pos, *_weights(wq, wk, q.shape[-1], q), eps, oq, ok,
+                                     _stream(q.device)))
+        return out
+
+    def norm_backward(self, dq_out, dk_out, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
+        """(dq, dk, dwq, dwk) of :meth:`norm_apply`; dwq and dwk are float32 [dim].  ``out`` may be (dq_out, dk_out)."""
+        import torch
+        hq, hk, shape = self._shape(q, k)
+        gq = _heads("dq_out", dq_out, q, q.shape[:-2], q.shape[-2], q.shape[-1])
+        gk = _heads("dk_out", dk_out, q, k.shape[:-2], k.shape[-2], k.shape[-1])
+        pos = _ints("positions", positions, q.shape[:-2], torch.int64, q.device)
+        out, oq, ok = self._out(q, k, out)
+        dw = torch.empty(2, q.shape[-1], dtype=torch.float32, device=q.device)
+        n = lib.pn_norm_rotary_workspace(*shape[1:])
+        keep, ws = _workspace(n, q.device)
+        _ok(lib.pn_norm_rotary_backward(self.h, *shape, gq, gk, hq, hk, pos, *_weights(wq, wk, q.shape[-1], q), eps, oq,
+                                        ok, dw[0].data_ptr(), dw[1].data_ptr(), ws, n, _stream(q.device)))
+        return out[0], out[1], dw[0], dw[1]
+
+
+class LinearAttention:
+    """Linear attention with a decay for each head: S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t.
+
+    heads, kv_heads   query heads, and key and value heads (query head h reads key head h // (heads / kv_heads))
+    dk, dv            multiples of 8 up to 256
+    log_decay         [heads], finite and <= 0, on the host or a device (read once, here; no gradient is formed for it)
+    scale             None: dk ** -0.5
+    dtype             of q, k, v and o: torch.float32, bfloat16 or float16; states are float32
+    """
+
+    def __init__(self, heads: int, kv_heads: int, dk: int, dv: int, log_decay, scale: Optional[float] = None, dtype=None):
+        import torch
+        self.h = None
+        self.heads, self.kv_heads, self.dk, self.dv = int(heads), int(kv_heads), int(dk), int(dv)
+        self.dtype = torch.float32 if dtype is None else dtype
+        if self.dtype not in _dtypes():
+            raise ValueError(f"dtype {dtype}: float32, bfloat16 or float16 is wanted")
+        if isinstance(log_decay, torch.Tensor):
+            if log_decay.requires_grad:
+                raise ValueError("log_decay requires a gradient: the decays are fixed, detach it")
+            log_decay = log_decay.cpu().numpy()
+        g = np.ascontiguousarray(log_decay, dtype=np.float32)
+        if g.shape != (self.heads,):
+            raise ValueError(f"log_decay has shape {g.shape}; ({self.heads},) is wanted")
+        self.scale = float(dk) ** -0.5 if scale is None else float(scale)
+        h = ctypes.c_void_p()
+        _ok(lib.pn_linattn_create(ctypes.byref(h), self.heads, self.kv_heads, self.dk, self.dv, _dtypes()[self.dtype],
+                                  g.ctypes.data, self.scale))
+        self.h = h.value
+
+    def __del__(self):
+        if getattr(self, "h", None):
+            lib.pn_linattn_destroy(self.h)
+            self.h = None
+
+    def _operands(self, q, k, v):
+        if q.dtype != self.dtype:
+            raise ValueError(f"q is {q.dtype}; {self.dtype} is wanted")
+        lead = q.shape[:-2]
+        return (_heads("q", q, q, lead, self.heads, self.dk), _heads("k", k, q, lead, self.kv_heads, self.dk),
+                _heads("v", v, q, lead, self.kv_heads, self.dv))
+
+    def _sequences(self, q, cu_seqlens, max_len):
+        """(n_seq, T, cu pointer, max_len) of the rows."""
+        import torch
+        if cu_seqlens is None:
+            n, T = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
+            return n, T, None, 0
+        if q.dim() != 3:
+            raise ValueError("packed sequences (cu_seqlens) are [tokens, heads, dim]")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [sequences + 1]")
+        return (cu_seqlens.numel() - 1, q.shape[0],
+                _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, q.device), int(max_len or 0))
+
+    def forward(self, q, k, v, initial_state=None, cu_seqlens=None, max_len: Optional[int] = None, out=None):
+        """(o, final state) of whole sequences.
+
+        q [batch, tokens, heads, dk], k and v with kv_heads; or, with ``cu_seqlens`` (int32 [sequences + 1], on the
+        device), packed [rows, heads, dk], where rows before the first and behind the last sequence are neither read nor
+        written.  ``max_len``: the longest sequence, a hint for the work's split.  States: float32
+        [sequences, heads, dk, dv].  ``out``: a tensor for o."""
+        import torch
+        hq, hk, hv = self._operands(q, k, v)
+        n, T, cu, max_len = self._sequences(q, cu_seqlens, max_len)
+        shape = (n, self.heads, self.dk, self.dv)
+        s0 = _float32("initial_state", initial_state, shape, q.device)
+        state = torch.empty(shape, dtype=torch.float32, device=q.device)
+        if out is None:
+            out = torch.empty(*q.shape[:-1], self.dv, dtype=q.dtype, device=q.device)
+        ho = _heads("out", out, q, q.shape[:-2], self.heads, self.dv)
+        _distinct("out", out)
+        size = lib.pn_linattn_workspace(self.h, 0, n, T, cu is not None, max_len)
+        keep, ws = _workspace(size, q.device)
+        _ok(lib.pn_linattn_forward(self.h, n, T, cu, max_len, hq, hk, hv, s0, ho, state.data_ptr(), ws, size,
+                                   _stream(q.device)))
+        return out, state
+
+    def backward(self, do, q, k, v, initial_state=None, dstate=None, cu_seqlens=None, max_len: Optional[int] = None,
+                 grads=None):
+        """(dq, dk, dv, gradient of the initial state) of :meth:`forward` with the same inputs, from the gradients of o
+        and (None: zero) of the final state.  ``grads``: a triple of tensors for dq, dk and dv."""
+        import torch
+        hq, hk, hv = self._operands(q, k, v)
+        n, T, cu, max_len = self._sequences(q, cu_seqlens, max_len)
+        shape = (n, self.heads, self.dk, self.dv)
+        hdo = _heads("do", do, q, q.shape[:-2], self.heads, self.dv)
+        s0 = _float32("initial_state", initial_state, shape, q.device)
+        ds = _float32("dstate", dstate, shape, q.device)
+        if grads is None:
+            grads = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
+        dq, dk, dv = grads
+        outs = []
+        for name, t, like in (("grads[0]", dq, q), ("grads[1]", dk, k), ("grads[2]", dv, v)):
+            outs.append(_heads(name, t, q, like.shape[:-2], like.shape[-2], like.shape[-1]))
+            _distinct(name, t)
+        ds0 = torch.empty(shape, dtype=torch.float32, device=q.device)
+        size = lib.pn_linattn_workspace(self.h, 1, n, T, cu is not None, max_len)
+        keep, ws = _workspace(size, q.device)
+        _ok(lib.pn_linattn_backward(self.h, n, T, cu, max_len, hdo, hq, hk, hv, s0, ds, *outs, ds0.data_ptr(), ws, size,
+                                    _stream(q.device)))
+        return dq, dk, dv, ds0
+
+    def step(self, q, k, v, states, slots=None, rotary: Optional[Rotary] = None, positions=None, wq=None, wk=None,
+             eps: float = 1e-6, out=None):
+        """o [rows, heads, dv] of one token of each of the rows; ``states`` [slots, heads, dk, dv] is updated in place.
+
+        q [rows, heads, dk], k and v with kv_heads.  ``slots``: int64 [rows], the state of each row (None: row b has
+        state b); a slot outside the states, or one that an earlier row names, makes its row padding, which is left as it
+        is (in ``out`` too; without ``out`` such rows are undefined).  ``wq``, ``wk``: the norm of q and k, ``rotary``
+        with ``positions`` (int64 [rows]): their rotation, both in the same pass."""
+        import torch
+        if q.dim() != 3:
+            raise ValueError("q must be [rows, heads, dk]")
+        ops = self._operands(q, k, v)
+        if out is None:
+            out = torch.empty(q.shape[0], self.heads, self.dv, dtype=q.dtype, device=q.device)
+        ops += (_heads("out", out, q, q.shape[:-2], self.heads, self.dv),)
+        _distinct("out", out)
+        if states.dim() != 4:
+            raise ValueError("states must be [slots, heads, dk, dv]")
+        n = states.shape[0]
+        st = _float32("states", states, (n, self.heads, self.dk, self.dv), q.device)
+        sl = None if slots is None else _ints("slots", slots, (q.shape[0],), torch.int64, q.device)
+        if (wq is None) != (wk is None):
+            raise ValueError("wq and wk come together")
+        w = (None, None, PN_F32) if wq is None else _weights(wq, wk, self.dk, q)
+        if (rotary is None) != (positions is None):
+            raise ValueError("rotary and positions come together")
+        pos = None if rotary is None else _ints("positions", positions, (q.shape[0],), torch.int64, q.device)
+        for x in ops:   # rows lie at the batch stride
+            x.batch_stride = x.token_stride
+        _ok(lib.pn_linattn_step(self.h, q.shape[0], *ops, st, n, sl, rotary.h if rotary is not None else None, pos, *w,
+                                eps, _stream(q.device)))
+        return out

@@ -1,0 +1,372 @@
+// pn_linattn.cu -- entry points of linear attention with a decay for each head.
+#include <algorithm>
+#include <cmath>
+#include <memory>
+
+#include "pn_linattn.cuh"
+
+namespace pn {
+namespace {
+
+pn_status check_op(const pn_heads* x, const char* name, size_t es, int* dev, bool empty) {
+  if (!x) return seq_fail(PN_ERR_INVALID, "%s is NULL", name);
+  if (x->batch_stride < 0 || x->token_stride < 0 || x->head_stride < 0)
+    return seq_fail(PN_ERR_INVALID, "%s has a negative stride", name);
+  if (empty) return PN_OK;
+  if (pn_status e = seq_device(x->data, name, dev)) return e;
+  if ((uintptr_t)x->data % es) return seq_fail(PN_ERR_INVALID, "%s is misaligned", name);
+  return PN_OK;
+}
+
+pn_status check_f32(const void* p, const char* name, int* dev) {
+  if (!p) return PN_OK;
+  if (pn_status e = seq_device(p, name, dev)) return e;
+  if ((uintptr_t)p & 15u) return seq_fail(PN_ERR_INVALID, "%s must be 16-byte aligned", name);
+  return PN_OK;
+}
+
+LinOperand operand(const pn_heads* x, int per) {
+  return LinOperand{x->data, x->batch_stride, x->token_stride, x->head_stride, per};
+}
+
+// Rows of one chunk of the FP32 kernels.
+int fma_chunk(int da) { return da <= 128 ? 64 : 32; }
+
+// Parts a sequence is cut into: enough CTAs for the card where sequences and heads are few, at least
+// four chunks each (a part costs a second read of two operands).
+int fma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int dc) {
+  const long long ctas = (long long)n_seq * h->H * ((dc + kLinDC - 1) / kLinDC);
+  const long long want = (2 * 148 + ctas - 1) / std::max(1LL, ctas);
+  const long long most = max_len / (4 * fma_chunk(da));
+  return (int)std::max(1LL, std::min(want, most));
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t seg_bytes(const pn_linattn_s* h, int n_seq, long long max_len) {
+  const int p = std::max(fma_parts(h, n_seq, max_len, h->dk, h->dv), fma_parts(h, n_seq, max_len, h->dv, h->dk));
+  return p > 1 ? align256((size_t)n_seq * h->H * p * h->dk * h->dv * sizeof(float)) : 0;
+}
+
+template <typename T, int C, int DA>
+cudaError_t launch_fma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
+  using K = LinFmaCfg<C, DA>;
+  const dim3 grid((P.dc + kLinDC - 1) / kLinDC, P.nseg, P.n_seq * P.H);
+  cudaError_t e;
+  if (P.nseg > 1) {
+    if ((e = cudaFuncSetAttribute(lin_fma_kernel<T, C, DA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  K::SMEM_BYTES)) != cudaSuccess)
+      return e;
+    lin_fma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), kLinThreads, K::SMEM_BYTES, st>>>(P, G);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, C);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if ((e = cudaFuncSetAttribute(lin_fma_kernel<T, C, DA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                K::SMEM_BYTES)) != cudaSuccess)
+    return e;
+  lin_fma_kernel<T, C, DA, false><<<grid, kLinThreads, K::SMEM_BYTES, st>>>(P, G);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_pass(const LinPass& P, const LinDecay& G, cudaStream_t st) {
+  if (P.da <= 64) return launch_fma<T, 64, 64>(P, G, st);
+  if (P.da <= 128) return launch_fma<T, 64, 128>(P, G, st);
+  return launch_fma<T, 32, 256>(P, G, st);
+}
+
+// One pass over every sequence and head.
+cudaError_t run_pass(const pn_linattn_s* h, LinPass P, int n_seq, long long max_len, void* seg, cudaStream_t st) {
+  LinDecay G;
+  std::copy(h->log2_decay, h->log2_decay + h->H, G.log2);
+  P.H = h->H;
+  P.n_seq = n_seq;
+  P.nseg = fma_parts(h, n_seq, max_len, P.da, P.dc);
+  P.seg_state = (float*)seg;
+  switch (h->dtype) {
+    case PN_F32: return launch_pass<float>(P, G, st);
+    case PN_BF16: return launch_pass<__nv_bfloat16>(P, G, st);
+    default: return launch_pass<__half>(P, G, st);
+  }
+}
+
+template <typename T>
+cudaError_t group_sum(const float* part, long long rows, int H, int G, int d, const pn_heads* dst, long long tokens,
+                      const int* cu, int n_seq, cudaStream_t st) {
+  const long long n = rows * (H / G) * d;
+  const int grid = (int)std::min<long long>((n + 255) / 256, 148LL * 16);
+  lin_group_sum_kernel<T><<<grid, 256, 0, st>>>(part, rows, H, G, d, (T*)dst->data, dst->batch_stride, dst->token_stride,
+                                               dst->head_stride, tokens, cu, n_seq);
+  return cudaGetLastError();
+}
+
+struct Shape {
+  long long rows;      // of the buffers
+  long long tokens;    // rows of a batch entry (ragged: all rows)
+  long long max_len;
+};
+
+pn_status check_shape(const pn_linattn_s* h, int n_seq, long long T, const int* cu, long long max_len, Shape* s) {
+  if (!h) return seq_fail(PN_ERR_INVALID, "handle is NULL");
+  if (n_seq < 0 || T < 0) return seq_fail(PN_ERR_INVALID, "bad shape n_seq=%d T=%lld", n_seq, T);
+  if (T > 0x7fffff00LL) return seq_fail(PN_ERR_INVALID, "T=%lld: at most 2^31 - 256 rows", T);
+  if ((long long)n_seq * h->H > 65535) return seq_fail(PN_ERR_INVALID, "n_seq * heads = %lld: at most 65535", (long long)n_seq * h->H);
+  if (max_len < 0) return seq_fail(PN_ERR_INVALID, "max_len must be >= 0");
+  s->rows = cu ? T : n_seq * T;
+  s->tokens = T;
+  s->max_len = cu ? (max_len > 0 ? std::min(max_len, T) : T) : T;
+  return PN_OK;
+}
+
+}  // namespace
+}  // namespace pn
+
+using namespace pn;
+
+extern "C" {
+
+pn_status pn_linattn_create(pn_linattn* out, int H, int Hkv, int dk, int dv, int dtype, const float* log_decay, float scale) {
+  if (!out) return seq_fail(PN_ERR_INVALID, "out is NULL");
+  *out = nullptr;
+  if (H < 1 || H > kMaxLinHeads) return seq_fail(PN_ERR_INVALID, "H=%d: from 1 to %d", H, kMaxLinHeads);
+  if (Hkv < 1 || H % Hkv) return seq_fail(PN_ERR_INVALID, "Hkv=%d does not divide H=%d", Hkv, H);
+  for (int d : {dk, dv})
+    if (d < 8 || d > 256 || d % 8) return seq_fail(PN_ERR_INVALID, "dk=%d dv=%d: multiples of 8 from 8 to 256", dk, dv);
+  if (dtype != PN_F32 && dtype != PN_BF16 && dtype != PN_F16) return seq_fail(PN_ERR_INVALID, "unknown dtype %d", dtype);
+  if (!log_decay) return seq_fail(PN_ERR_INVALID, "log_decay is NULL");
+  if (!std::isfinite(scale)) return seq_fail(PN_ERR_INVALID, "scale must be finite");
+  for (int i = 0; i < H; ++i)
+    if (!std::isfinite(log_decay[i]) || log_decay[i] > 0.0f)
+      return seq_fail(PN_ERR_INVALID, "log_decay[%d]=%g: finite and <= 0", i, (double)log_decay[i]);
+  pn_linattn_s* h = new (std::nothrow) pn_linattn_s();
+  if (!h) return seq_fail(PN_ERR_NOMEM, "out of host memory");
+  h->H = H;
+  h->Hkv = Hkv;
+  h->dk = dk;
+  h->dv = dv;
+  h->dtype = dtype;
+  h->scale = scale;
+  for (int i = 0; i < H; ++i) h->log2_decay[i] = (float)((double)log_decay[i] * 1.4426950408889634074);
+  *out = h;
+  return PN_OK;
+}
+
+void pn_linattn_destroy(pn_linattn h) { delete h; }
+
+size_t pn_linattn_workspace(pn_linattn h, int backward, int n_seq, long long T, int ragged, long long max_len) {
+  if (!h || n_seq < 1 || T < 1) return 0;
+  const long long len = ragged && max_len > 0 ? std::min(max_len, T) : T;
+  size_t n = seg_bytes(h, n_seq, len);
+  if (backward && h->H > h->Hkv)
+    n += align256((size_t)(ragged ? T : n_seq * T) * h->H * std::max(h->dk, h->dv) * sizeof(float));
+  return n;
+}
+
+pn_status pn_linattn_forward(pn_linattn h, int n_seq, long long T, const int* cu_seqlens, long long max_len,
+                             const pn_heads* q, const pn_heads* k, const pn_heads* v, const float* initial_state,
+                             const pn_heads* o, float* final_state, void* workspace, size_t workspace_bytes,
+                             void* cuda_stream) {
+  Shape s;
+  if (pn_status e = check_shape(h, n_seq, T, cu_seqlens, max_len, &s)) return e;
+  int dev = -1;
+  const size_t es = dtype_size(h->dtype);
+  const bool empty = s.rows == 0;
+  const pn_heads* ops[] = {q, k, v, o};
+  const char* names[] = {"q", "k", "v", "o"};
+  for (int i = 0; i < 4; ++i)
+    if (pn_status e = check_op(ops[i], names[i], es, &dev, empty)) return e;
+  if (pn_status e = check_f32(initial_state, "initial_state", &dev)) return e;
+  if (pn_status e = check_f32(final_state, "final_state", &dev)) return e;
+  if (cu_seqlens)
+    if (pn_status e = seq_device(cu_seqlens, "cu_seqlens", &dev)) return e;
+  if (n_seq == 0 || (empty && !final_state)) return PN_OK;
+  const size_t need = pn_linattn_workspace(h, 0, n_seq, T, cu_seqlens != nullptr, max_len);
+  if (workspace_bytes < need) return seq_fail(PN_ERR_INVALID, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (need)
+    if (pn_status e = check_f32(workspace, "workspace", &dev)) return e;
+  if (need && !workspace) return seq_fail(PN_ERR_INVALID, "workspace is NULL");
+  SeqDeviceGuard dg(dev);
+  const int G = h->H / h->Hkv;
+  LinPass P = {};
+  P.a = operand(q, 1);
+  P.b = operand(k, G);
+  P.c = operand(v, G);
+  P.out = o->data;
+  P.out_bs = o->batch_stride;
+  P.out_ts = o->token_stride;
+  P.out_hs = o->head_stride;
+  P.da = h->dk;
+  P.dc = h->dv;
+  P.T = T;
+  P.cu = cu_seqlens;
+  P.alpha = 1.0f;
+  P.beta = h->scale;
+  P.s_in = initial_state;
+  P.s_out = final_state;
+  P.s_row = h->dv;
+  P.s_col = 1;
+  const cudaError_t e = run_pass(h, P, n_seq, s.max_len, workspace, (cudaStream_t)cuda_stream);
+  if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+  return PN_OK;
+}
+
+pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const int* cu_seqlens, long long max_len,
+                              const pn_heads* d_o, const pn_heads* q, const pn_heads* k, const pn_heads* v,
+                              const float* initial_state, const float* d_final_state, const pn_heads* dq,
+                              const pn_heads* dk, const pn_heads* dv, float* d_initial_state, void* workspace,
+                              size_t workspace_bytes, void* cuda_stream) {
+  Shape s;
+  if (pn_status e = check_shape(h, n_seq, T, cu_seqlens, max_len, &s)) return e;
+  int dev = -1;
+  const size_t es = dtype_size(h->dtype);
+  const bool empty = s.rows == 0;
+  const pn_heads* ops[] = {d_o, q, k, v, dq, dk, dv};
+  const char* names[] = {"d_o", "q", "k", "v", "dq", "dk", "dv"};
+  for (int i = 0; i < 7; ++i)
+    if (pn_status e = check_op(ops[i], names[i], es, &dev, empty)) return e;
+  if (pn_status e = check_f32(initial_state, "initial_state", &dev)) return e;
+  if (pn_status e = check_f32(d_final_state, "d_final_state", &dev)) return e;
+  if (pn_status e = check_f32(d_initial_state, "d_initial_state", &dev)) return e;
+  if (cu_seqlens)
+    if (pn_status e = seq_device(cu_seqlens, "cu_seqlens", &dev)) return e;
+  if (n_seq == 0 || (empty && !d_initial_state)) return PN_OK;
+  const size_t need = pn_linattn_workspace(h, 1, n_seq, T, cu_seqlens != nullptr, max_len);
+  if (workspace_bytes < need) return seq_fail(PN_ERR_INVALID, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  if (need)
+    if (pn_status e = check_f32(workspace, "workspace", &dev)) return e;
+  if (need && !workspace) return seq_fail(PN_ERR_INVALID, "workspace is NULL");
+  SeqDeviceGuard dg(dev);
+  cudaStream_t st = (cudaStream_t)cuda_stream;
+  const int G = h->H / h->Hkv;
+  float* part = G > 1 ? (float*)((char*)workspace + seg_bytes(h, n_seq, s.max_len)) : nullptr;
+  cudaError_t e = cudaSuccess;
+
+  LinPass P = {};
+  P.T = T;
+  P.cu = cu_seqlens;
+  if (!empty) {
+    // dq_t = scale S_t do_t
+    P.a = operand(d_o, 1);
+    P.b = operand(v, G);
+    P.c = operand(k, G);
+    P.out = dq->data;
+    P.out_bs = dq->batch_stride;
+    P.out_ts = dq->token_stride;
+    P.out_hs = dq->head_stride;
+    P.da = h->dv;
+    P.dc = h->dk;
+    P.alpha = 1.0f;
+    P.beta = h->scale;
+    P.s_in = initial_state;
+    P.s_row = 1;
+    P.s_col = h->dv;
+    e = run_pass(h, P, n_seq, s.max_len, workspace, st);
+  }
+  // against time, G_t = scale q_t do_t^T + e^g G_{t+1}: dk_t = G_t v_t, dv_t = G_t^T k_t, dS_0 = e^g G_1
+  P.reverse = 1;
+  P.alpha = h->scale;
+  P.beta = 1.0f;
+  P.s_in = d_final_state;
+  P.out_f32 = G > 1;
+  for (int which = 0; which < 2 && e == cudaSuccess; ++which) {
+    const pn_heads* dst = which ? dv : dk;
+    const int d = which ? h->dv : h->dk;
+    if (which == 0 && empty) continue;
+    P.a = operand(which ? k : v, G);
+    P.b = which ? operand(q, 1) : operand(d_o, 1);
+    P.c = which ? operand(d_o, 1) : operand(q, 1);
+    P.da = which ? h->dk : h->dv;
+    P.dc = which ? h->dv : h->dk;
+    P.s_row = which ? h->dv : 1;
+    P.s_col = which ? 1 : h->dv;
+    P.s_out = which ? d_initial_state : nullptr;
+    P.out = G > 1 ? part : dst->data;
+    P.out_bs = G > 1 ? T * h->H * d : dst->batch_stride;
+    P.out_ts = G > 1 ? (long long)h->H * d : dst->token_stride;
+    P.out_hs = G > 1 ? d : dst->head_stride;
+    e = run_pass(h, P, n_seq, s.max_len, workspace, st);
+    if (G > 1 && e == cudaSuccess && !empty) {
+      e = h->dtype == PN_F32    ? group_sum<float>(part, s.rows, h->H, G, d, dst, T, cu_seqlens, n_seq, st)
+          : h->dtype == PN_BF16 ? group_sum<__nv_bfloat16>(part, s.rows, h->H, G, d, dst, T, cu_seqlens, n_seq, st)
+                                : group_sum<__half>(part, s.rows, h->H, G, d, dst, T, cu_seqlens, n_seq, st);
+    }
+  }
+  if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+  return PN_OK;
+}
+
+pn_status pn_linattn_step(pn_linattn h, int rows, const pn_heads* q, const pn_heads* k, const pn_heads* v, const pn_heads* o,
+                          float* states, long long n_slots, const long long* slots, pn_rotary r, const long long* positions,
+                          const void* wq, const void* wk, int w_dtype, float eps, void* cuda_stream) {
+  if (!h) return seq_fail(PN_ERR_INVALID, "handle is NULL");
+  if (rows < 0 || rows > 65535) return seq_fail(PN_ERR_INVALID, "rows=%d: from 0 to 65535", rows);
+  if (n_slots < 0) return seq_fail(PN_ERR_INVALID, "n_slots must be >= 0");
+  if (!slots && rows > n_slots) return seq_fail(PN_ERR_INVALID, "rows=%d exceeds n_slots=%lld", rows, n_slots);
+  if ((wq == nullptr) != (wk == nullptr)) return seq_fail(PN_ERR_INVALID, "wq and wk come together");
+  if (wq && w_dtype != PN_F32 && w_dtype != h->dtype) return seq_fail(PN_ERR_INVALID, "weights: float32 or the tensors' type");
+  if (wq && (!(eps >= 0.0f) || !std::isfinite(eps))) return seq_fail(PN_ERR_INVALID, "eps must be finite and >= 0");
+  if (r && 2 * r->pairs > h->dk) return seq_fail(PN_ERR_INVALID, "rot_dim=%d exceeds dk=%d", 2 * r->pairs, h->dk);
+  int dev = -1;
+  const size_t es = dtype_size(h->dtype);
+  const pn_heads* ops[] = {q, k, v, o};
+  const char* names[] = {"q", "k", "v", "o"};
+  for (int i = 0; i < 4; ++i)
+    if (pn_status e = check_op(ops[i], names[i], es, &dev, rows == 0)) return e;
+  if (rows == 0 || n_slots == 0) return PN_OK;
+  if (!states) return seq_fail(PN_ERR_INVALID, "states is NULL");
+  if (pn_status e = check_f32(states, "states", &dev)) return e;
+  if (slots)
+    if (pn_status e = seq_device(slots, "slots", &dev)) return e;
+  if (r)
+    if (pn_status e = seq_device(positions, "positions", &dev)) return e;
+  if (wq) {
+    if (pn_status e = seq_device(wq, "wq", &dev)) return e;
+    if (pn_status e = seq_device(wk, "wk", &dev)) return e;
+  }
+  SeqDeviceGuard dg(dev);
+  const int G = h->H / h->Hkv;
+  LinStep P = {};
+  P.q = operand(q, 1);
+  P.k = operand(k, G);
+  P.v = operand(v, G);
+  P.o = o->data;
+  P.o_bs = o->batch_stride;
+  P.o_hs = o->head_stride;
+  P.H = h->H;
+  P.dk = h->dk;
+  P.dv = h->dv;
+  P.scale = h->scale;
+  P.states = states;
+  P.n_slots = n_slots;
+  P.slots = slots;
+  P.positions = positions;
+  P.wq = wq;
+  P.wk = wk;
+  P.w_f32 = w_dtype == PN_F32;
+  P.eps = eps;
+  if (r) {
+    P.pairs = r->pairs;
+    P.interleaved = r->interleaved;
+    P.m = r->factor;
+    std::copy(r->turn, r->turn + r->pairs, P.turn);
+  }
+  LinDecay D;
+  std::copy(h->log2_decay, h->log2_decay + h->H, D.log2);
+  cudaStream_t st = (cudaStream_t)cuda_stream;
+  // narrow columns (32) while that many CTAs fit the card at once, else 128 columns
+  const bool narrow = (long long)rows * h->H * ((h->dv + 31) / 32) <= 148 * 4;
+  const int w = narrow ? 32 : 128;
+  const dim3 grid((h->dv + w - 1) / w, h->H, rows);
+  auto go = [&](auto tag) {
+    using T = decltype(tag);
+    if (narrow) lin_step_kernel<T, 8><<<grid, kStepThreads, 0, st>>>(P, D);
+    else lin_step_kernel<T, 32><<<grid, kStepThreads, 0, st>>>(P, D);
+    return cudaGetLastError();
+  };
+  const cudaError_t e = h->dtype == PN_F32 ? go(float{}) : h->dtype == PN_BF16 ? go(__nv_bfloat16{}) : go(__half{});
+  if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+  return PN_OK;
+}
+
+}  // extern "C"
