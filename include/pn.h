@@ -481,6 +481,12 @@ PN_API pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const
                                      const pn_heads* dv, float* d_initial_state, void* workspace,
                                      size_t workspace_bytes, void* cuda_stream);
 
+/* Waits for the stream, then reports whether a bounded device wait of pn_linattn_forward or
+ * pn_linattn_backward on the current device has given up since the last check (PN_ERR_TIMEOUT: what those
+ * calls wrote is invalid; the report is cleared).  No call is known to do so; the calls themselves do not wait
+ * and cannot tell. */
+PN_API pn_status pn_linattn_check(void* cuda_stream);
+
 /* One token of each of `rows` (<= 65535) sequences, in one launch: the states are updated in place.
  *   q, k, v, o  row b at batch_stride (token_stride ignored)
  *   states      device [n_slots][H][dk][dv], 16-byte aligned

@@ -310,6 +310,14 @@ class LinearAttention:
                                     _stream(q.device)))
         return dq, dk, dv, ds0
 
+    @staticmethod
+    def check(device=None):
+        """Wait for the current stream and raise where a bounded device wait of a forward or backward pass on the device has
+        given up since the last check (its results are invalid).  The passes are asynchronous and cannot tell."""
+        import torch
+        with torch.cuda.device(device):
+            _ok(lib.pn_linattn_check(torch.cuda.current_stream().cuda_stream))
+
     def step(self, q, k, v, states, slots=None, rotary: Optional[Rotary] = None, positions=None, wq=None, wk=None,
              eps: float = 1e-6, out=None):
         """o [rows, heads, dv] of one token of each of the rows; ``states`` [slots, heads, dk, dv] is updated in place.

@@ -1049,6 +1049,15 @@ pn_status select_kernels(pn_ctx* h) {
 }  // namespace
 
 namespace pn {
+// A tensor map of 128-byte swizzled boxes.
+CUresult encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, unsigned rank, const void* base, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  const cuuint32_t ones[5] = {1u, 1u, 1u, 1u, 1u};
+  return fn(m, type, rank, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
 // Sets the calling thread's handle-less error message (pn_last_error(NULL)).
 void set_thread_error(const char* msg) { g_create_error = msg ? msg : ""; }
 

@@ -3,9 +3,11 @@
 #include <cmath>
 #include <memory>
 
-#include "pn_linattn.cuh"
+#include "pn_linattn_tc.cuh"
 
 namespace pn {
+CUresult encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, unsigned rank, const void* base, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box);   // pn_api.cu
 namespace {
 
 pn_status check_op(const pn_heads* x, const char* name, size_t es, int* dev, bool empty) {
@@ -41,10 +43,22 @@ int fma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int d
   return (int)std::max(1LL, std::min(want, most));
 }
 
+// Parts for the tensor-core kernel: a CTA fills its SM, so as many as fit the card beside each other.
+int tc_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int dc) {
+  const long long ctas = (long long)n_seq * h->H * ((dc + 127) / 128);
+  const long long want = 148 / std::max(1LL, ctas);
+  return (int)std::max(1LL, std::min(want, max_len / (4 * 64)));
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t seg_bytes(const pn_linattn_s* h, int n_seq, long long max_len) {
-  const int p = std::max(fma_parts(h, n_seq, max_len, h->dk, h->dv), fma_parts(h, n_seq, max_len, h->dv, h->dk));
+  // the largest of what either kernel takes in either direction (which one runs goes by the arrays' alignment)
+  int p = 1;
+  for (int t = 0; t < 2; ++t) {
+    const int da = t ? h->dv : h->dk, dc = t ? h->dk : h->dv;
+    p = std::max(p, std::max(fma_parts(h, n_seq, max_len, da, dc), tc_parts(h, n_seq, max_len, da, dc)));
+  }
   return p > 1 ? align256((size_t)n_seq * h->H * p * h->dk * h->dv * sizeof(float)) : 0;
 }
 
@@ -59,7 +73,7 @@ cudaError_t launch_fma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
       return e;
     lin_fma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), kLinThreads, K::SMEM_BYTES, st>>>(P, G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, C);
+    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, C, 0);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = cudaFuncSetAttribute(lin_fma_kernel<T, C, DA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -76,14 +90,71 @@ cudaError_t launch_pass(const LinPass& P, const LinDecay& G, cudaStream_t st) {
   return launch_fma<T, 32, 256>(P, G, st);
 }
 
+// The tensor map of one operand: boxes of 64 rows x 64 columns of one head, 128-byte swizzled.
+// False where TMA cannot read it (alignment, strides).
+bool encode_operand(CUtensorMap* m, const LinOperand& x, int width, int heads, long long T, int batch) {
+  if ((uintptr_t)x.p & 15u) return false;
+  const cuuint64_t row = ((cuuint64_t)width * 2 + 15) / 16 * 16;
+  cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)T, (cuuint64_t)batch};
+  const long long es[3] = {x.hs, x.ts, x.bs};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) {
+    const bool one = dims[i + 1] == 1;   // a stride that is never taken
+    if (!one && (es[i] <= 0 || es[i] % 8 || es[i] * 2 >= (1LL << 40))) return false;
+    strides[i] = one ? row : (cuuint64_t)es[i] * 2;
+  }
+  const cuuint32_t box[4] = {64, 1, 64, 1};
+  return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, x.p, dims, strides, box) == CUDA_SUCCESS;
+}
+
+template <typename T, int DA, int DC>
+cudaError_t launch_tc(const LinMaps& maps, const LinPass& P, const LinDecay& G, cudaStream_t st) {
+  using K = LinTcCfg<DA, DC>;
+  const dim3 grid((P.dc + DC - 1) / DC, P.n_seq * P.H, P.nseg);
+  cudaError_t e;
+  if (P.nseg > 1) {
+    if ((e = cudaFuncSetAttribute(lin_tc_kernel<T, DA, DC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  K::SMEM_BYTES)) != cudaSuccess)
+      return e;
+    lin_tc_kernel<T, DA, DC, true><<<dim3(grid.x, grid.y, P.nseg - 1), K::NT, K::SMEM_BYTES, st>>>(maps, P, G);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, K::C, 1);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if ((e = cudaFuncSetAttribute(lin_tc_kernel<T, DA, DC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                K::SMEM_BYTES)) != cudaSuccess)
+    return e;
+  lin_tc_kernel<T, DA, DC, false><<<grid, K::NT, K::SMEM_BYTES, st>>>(maps, P, G);
+  return cudaGetLastError();
+}
+
+// The tensor-core kernel, where it can take the pass; false where the FP32 kernel has to.
+bool try_tc(const pn_linattn_s* h, LinPass& P, const LinDecay& G, long long max_len, cudaStream_t st, cudaError_t* e) {
+  if (h->dtype != PN_BF16 || P.da > 128 || P.T < 1) return false;
+  LinMaps maps;
+  const int batch = P.cu ? 1 : P.n_seq;
+  if (!encode_operand(&maps.a, P.a, P.da, P.H / P.a.per, P.T, batch) ||
+      !encode_operand(&maps.b, P.b, P.da, P.H / P.b.per, P.T, batch) ||
+      !encode_operand(&maps.c, P.c, P.dc, P.H / P.c.per, P.T, batch))
+    return false;
+  P.out_map = !P.out_f32 && encode_operand(&maps.o, LinOperand{P.out, P.out_bs, P.out_ts, P.out_hs, 1}, P.dc, P.H, P.T, batch);
+  P.nseg = tc_parts(h, P.n_seq, max_len, P.da, P.dc);
+  using T = __nv_bfloat16;
+  if (P.da <= 64) *e = P.dc <= 64 ? launch_tc<T, 64, 64>(maps, P, G, st) : launch_tc<T, 64, 128>(maps, P, G, st);
+  else *e = P.dc <= 64 ? launch_tc<T, 128, 64>(maps, P, G, st) : launch_tc<T, 128, 128>(maps, P, G, st);
+  return true;
+}
+
 // One pass over every sequence and head.
 cudaError_t run_pass(const pn_linattn_s* h, LinPass P, int n_seq, long long max_len, void* seg, cudaStream_t st) {
   LinDecay G;
   std::copy(h->log2_decay, h->log2_decay + h->H, G.log2);
   P.H = h->H;
   P.n_seq = n_seq;
-  P.nseg = fma_parts(h, n_seq, max_len, P.da, P.dc);
   P.seg_state = (float*)seg;
+  cudaError_t e;
+  if (try_tc(h, P, G, max_len, st, &e)) return e;
+  P.nseg = fma_parts(h, n_seq, max_len, P.da, P.dc);
   switch (h->dtype) {
     case PN_F32: return launch_pass<float>(P, G, st);
     case PN_BF16: return launch_pass<__nv_bfloat16>(P, G, st);
@@ -293,6 +364,18 @@ pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const int* c
     }
   }
   if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "launch failed: %s", cudaGetErrorString(e));
+  return PN_OK;
+}
+
+pn_status pn_linattn_check(void* cuda_stream) {
+  cudaStream_t st = (cudaStream_t)cuda_stream;
+  unsigned word = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&word, lin_error_word, sizeof word, 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && word) e = cudaMemcpyToSymbolAsync(lin_error_word, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess && word) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "reading the device's error word failed: %s", cudaGetErrorString(e));
+  if (word) return seq_fail(PN_ERR_TIMEOUT, "a device wait of linear attention gave up: results since the last check are invalid");
   return PN_OK;
 }
 

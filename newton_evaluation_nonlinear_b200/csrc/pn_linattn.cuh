@@ -36,6 +36,7 @@ struct LinPass {
   void* out;
   long long out_bs, out_ts, out_hs;
   int out_f32;             // out is float32 (partial gradients of shared heads)
+  int out_map;             // whole chunks of out are stored by TMA
   int da, dc;              // widths: a and b, c and out
   int H, n_seq;
   long long T;             // rows of a sequence (no cu), or of the whole buffer
@@ -295,9 +296,11 @@ __global__ void __launch_bounds__(kLinThreads) lin_fma_kernel(const __grid_const
 
 // What each part left becomes what enters the next: slot p holds what part
 // p - 1 left and receives E_p = e^{g rows_(p-1)} E_(p-1) + left_(p-1), E_0 the
-// caller's state, in order of the parts.
+// caller's state, in order of the parts.  `chunked`: parts are whole chunks of C in
+// the order of the rows even against time, so that the first part then has the short
+// chunk; else they are rows in the order they are taken.
 __global__ void __launch_bounds__(256) lin_combine_kernel(const __grid_constant__ LinPass P,
-                                                          const __grid_constant__ LinDecay G, int C) {
+                                                          const __grid_constant__ LinDecay G, int C, int chunked) {
   const int sh = blockIdx.y;
   const int h = sh % P.H, s = sh / P.H;
   const int e = blockIdx.x * 256 + threadIdx.x;
@@ -306,14 +309,16 @@ __global__ void __launch_bounds__(256) lin_combine_kernel(const __grid_constant_
   long long start;
   int len;
   lin_rows(P, s, start, len);
-  const int seg_len = lin_seg_len(len, P.nseg, C);
+  const int nch = (len + C - 1) / C;
+  const int seg_len = chunked ? (nch + P.nseg - 1) / P.nseg * C : lin_seg_len(len, P.nseg, C);
+  const int first = seg_len - (chunked && P.reverse ? nch * C - len : 0);   // rows of part 0, where others follow it
   const int i = e / P.dc, j = e % P.dc;
   float v = P.s_in ? P.s_in[(long long)sh * size + (long long)i * P.s_row + (long long)j * P.s_col] : 0.0f;
   float* at = P.seg_state + (long long)sh * P.nseg * size + e;
   at[0] = v;   // the parts read it here: the last one may overwrite the caller's state meanwhile
   const float f = lin_pow(G.log2[h], seg_len);
-  float f_in = P.reverse ? lin_pow(G.log2[h], seg_len - 1) : f;
-  for (int p = 1; p < P.nseg && (long long)p * seg_len < len; ++p) {
+  float f_in = lin_pow(G.log2[h], first - (P.reverse ? 1 : 0));
+  for (int p = 1; p < P.nseg && (long long)p * seg_len < (chunked ? (long long)nch * C : (long long)len); ++p) {
     v = fmaf(f_in, v, at[(long long)p * size]);
     at[(long long)p * size] = v;
     f_in = f;
