@@ -107,25 +107,25 @@ bool encode_operand(CUtensorMap* m, const LinOperand& x, int width, int heads, l
   return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, x.p, dims, strides, box) == CUDA_SUCCESS;
 }
 
+template <typename T, int DA, int DC, int WHAT>
+cudaError_t launch_tc_kernel(const LinMaps& maps, const LinPass& P, const LinDecay& G, unsigned parts, cudaStream_t st) {
+  using K = LinTcCfg<DA, DC>;
+  const cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<T, DA, DC, WHAT>, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  lin_tc_kernel<T, DA, DC, WHAT><<<dim3((P.dc + DC - 1) / DC, P.n_seq * P.H, parts), K::NT, K::SMEM_BYTES, st>>>(maps, P, G);
+  return cudaGetLastError();
+}
+
 template <typename T, int DA, int DC>
 cudaError_t launch_tc(const LinMaps& maps, const LinPass& P, const LinDecay& G, cudaStream_t st) {
-  using K = LinTcCfg<DA, DC>;
-  const dim3 grid((P.dc + DC - 1) / DC, P.n_seq * P.H, P.nseg);
-  cudaError_t e;
   if (P.nseg > 1) {
-    if ((e = cudaFuncSetAttribute(lin_tc_kernel<T, DA, DC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  K::SMEM_BYTES)) != cudaSuccess)
-      return e;
-    lin_tc_kernel<T, DA, DC, true><<<dim3(grid.x, grid.y, P.nseg - 1), K::NT, K::SMEM_BYTES, st>>>(maps, P, G);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, K::C, 1);
+    cudaError_t e = launch_tc_kernel<T, DA, DC, kLinStateOnly>(maps, P, G, P.nseg - 1, st);
+    if (e != cudaSuccess) return e;
+    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, LinTcCfg<DA, DC>::C, 1);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = cudaFuncSetAttribute(lin_tc_kernel<T, DA, DC, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                K::SMEM_BYTES)) != cudaSuccess)
-    return e;
-  lin_tc_kernel<T, DA, DC, false><<<grid, K::NT, K::SMEM_BYTES, st>>>(maps, P, G);
-  return cudaGetLastError();
+  return P.out_f32 ? launch_tc_kernel<T, DA, DC, kLinOutF32>(maps, P, G, P.nseg, st)
+                   : launch_tc_kernel<T, DA, DC, kLinOut>(maps, P, G, P.nseg, st);
 }
 
 // The tensor-core kernel, where it can take the pass; false where the FP32 kernel has to.

@@ -5,15 +5,19 @@
 // (sequence, head, part) and takes its chunks in turn; the state S^T (dc x da,
 // float32) never leaves the SM: it sits in TMEM.  Per chunk, all from operands that
 // TMA brought in 128-byte swizzled rows:
-//   P    = a b^T                          64 x 64     (times e^{g|i-j}|, masked, rounded: P~)
+//   P    = a b^T                          64 x 64     (masked, weighted, rounded: P~)
 //   O1^T = S~^T a^T                       dc x 64     (S~: S rounded to the operands' type)
 //   O2^T = c^T P~^T                       dc x 64
 //   U^T  = c'^T b                         dc x da     (c'_j = e^{g(n-1-j)} c_j)
 //   out_i = beta (e^{g(i+1)} O1_i + O2_i),   S = e^{gn} S + U.
+// O1 and O2 share one accumulator: with x_i = i + 1 the rows seen at row i and r = 32,
+//   out_i = beta e^{g(x_i - r)} [ (e^{gr} S) a_i + sum_j e^{g(r - x_j)} P_ij c_j ],
+// so P~ takes the weight e^{g(r - x_j)}, the state is kept times e^{gr}, and one factor a row is left
+// for the end.  It is the same sum times a power of e^g that is at most 2^40 either way where
+// |g| <= 1.25 ln 2 (e^g >= 0.42); heads that forget faster keep two accumulators.
 // The outputs are formed transposed, so that a TMEM lane is a column of c: a warp
 // writes 32 neighbouring outputs of a row, and the state's rows stay in their lanes.
-// The decay between the chunk's start and a row multiplies O1 after the product, in
-// float32, so no operand is rounded for it.  P~ and S~ are rounded once each to the
+// No operand is rounded for the decay alone.  P~ and S~ are rounded once each to the
 // operands' type: with u its half step, two relative errors of u on disjoint shares of
 // an output that is itself rounded by u.  The state, which accumulates over the whole
 // sequence and is returned in float32, takes c' in three pieces (c' = hi + mid + lo, 24
@@ -25,7 +29,7 @@
 // 128 x 128 x 64) 1600 clocks of its tensor cores; what must not add up is the work
 // between them.  So it is spread over warps that meet at mbarriers only:
 //   warp 0       TMA loads, NS chunks ahead
-//   warp 1       issues the products
+//   warps 1-3    issue the products: U; the outputs'; P
 //   warps 4-7    P -> P~
 //   warps 8-11   the outputs
 //   warps 12-19  S: the sum, in registers, and S~ (four warps for each half of its columns)
@@ -239,7 +243,7 @@ struct LinTcCfg {
   static constexpr int NP = 3;                             // pieces of c'
   static constexpr int O_BYTES = C * DC * 2;               // outputs on their way
   static constexpr bool TS = DC == 128;                    // the pieces lie in TMEM
-  static constexpr int CP_BYTES = TS ? 0 : NP * C_BYTES;
+  static constexpr int CP_BYTES = TS ? 0 : 2 * NP * C_BYTES;   // (twice, as in TMEM)
   static constexpr int FIXED = SB_BYTES + 2 * P_BYTES + CP_BYTES + O_BYTES;
   static constexpr int NSTAGE = (220 * 1024 - FIXED) / STAGE < 4 ? (220 * 1024 - FIXED) / STAGE : 4;
   static constexpr int OFF_SB = NSTAGE * STAGE;
@@ -247,28 +251,31 @@ struct LinTcCfg {
   static constexpr int OFF_CP = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_O = OFF_CP + CP_BYTES;
   static constexpr int SMEM_BYTES = OFF_O + O_BYTES + 1024;   // + alignment slack
-  static constexpr int COL_U = 0, COL_P = DA, COL_O2 = DA + 64, COL_O1 = DA + 128;   // O1 twice
-  static constexpr int COL_CP = DA + 256;                  // 32 columns a piece
+  static constexpr int COL_U = 0, COL_P = DA, COL_O = DA + 64;   // outputs twice: two chunks', or O1 and O2 of one
+  static constexpr int COL_CP = DA + 192;                  // twice 32 columns a piece
   static constexpr int TCOLS = 512;
-  static_assert(COL_CP + (TS ? 32 * NP : 0) <= TCOLS, "TMEM columns");
+  static_assert(COL_CP + (TS ? 2 * 32 * NP : 0) <= TCOLS, "TMEM columns");
   static_assert(NSTAGE >= 2, "two stages at least");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
-template <typename T, int DA, int DC, bool STATE_ONLY>
+enum { kLinOut, kLinOutF32, kLinStateOnly };   // what a pass writes: outputs of type T, float32 ones, states only
+
+template <typename T, int DA, int DC, int WHAT>
 __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinPass P,
                                                         const __grid_constant__ LinDecay G) {
   using K = LinTcCfg<DA, DC>;
   using X = Tc16<T>;
-  constexpr int C = K::C, NS = K::NSTAGE;
+  constexpr int C = K::C, NS = K::NSTAGE, R = C / 2;
+  constexpr bool STATE_ONLY = WHAT == kLinStateOnly;
   extern __shared__ __align__(1024) unsigned char smem_lt[];
   unsigned char* base = smem_lt + ((1024u - (smem_addr(smem_lt) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_pacc, bar_p, bar_s, bar_u, bar_ur, bar_o1, bar_cp, bar_oacc, bar_o, bar_done;
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_pacc, bar_p[2], bar_s, bar_u, bar_ur, bar_o1, bar_cp[2], bar_cpf[2], bar_zero, bar_oacc[2], bar_o[2], bar_done[3];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_loaded;
-  __shared__ __align__(16) float s_out[2][C];   // beta e^{g ..} of the state's share of row i: the first chunk, the others
-  __shared__ float s_w[C];                      // alpha e^{g n}
+  __shared__ __align__(16) float s_out[2][C];   // the factor of row i's outputs (two: of O1): the first chunk, the others
+  __shared__ float s_w[C];                      // the weight of column j of P (two: at |i - j|)
   __shared__ __align__(16) float s_c[C];        // the weights of c', from the far end of a whole chunk
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -295,33 +302,37 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&bar_full[i], 1u);
-      mbar_init(&bar_empty[i], 1u);
+      mbar_init(&bar_empty[i], STATE_ONLY ? 1u : 3u);
     }
     mbar_init(&bar_pacc, 1u);
-    mbar_init(&bar_p, 4u);
     mbar_init(&bar_s, 8u);
     mbar_init(&bar_u, 1u);
     mbar_init(&bar_ur, 8u);
+    mbar_init(&bar_zero, 8u);   // c is zero behind the last row (once, for the one short chunk there may be)
     mbar_init(&bar_o1, 1u);
-    mbar_init(&bar_cp, 8u);
-    mbar_init(&bar_oacc, 1u);
-    mbar_init(&bar_o, 4u);
-    mbar_init(&bar_done, 1u);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_cp[i], 8u);
+      mbar_init(&bar_cpf[i], 1u);
+      mbar_init(&bar_oacc[i], 1u);
+      mbar_init(&bar_o[i], 4u);
+      mbar_init(&bar_p[i], 4u);
+    }
+    for (int i = 0; i < 3; ++i) mbar_init(&bar_done[i], 1u);
     mbar_init_fence();
     s_abort = 0;
     s_loaded = 0;
   }
+  const bool two = !STATE_ONLY && !(l2 >= -1.25f);            // O1 and O2 apart
+  const float frame = STATE_ONLY || two ? 1.0f : exp2f(l2 * R);   // the state is kept times this
   if (tid < 2 * C) {
     const int which = tid / C, i = tid % C;
-    int n;
-    if (!P.reverse) n = i + 1;
-    else if (which == 0) n = (M > 0 ? rows_of(0) : C) - i - e0;
-    else n = C - i;
-    s_out[which][i] = P.beta * lin_pow(l2, n);
+    int n = P.reverse ? C - i : i + 1;
+    if (two && P.reverse && which == 0) n = (M > 0 ? rows_of(0) : C) - i - e0;
+    s_out[which][i] = P.beta * (two ? lin_pow(l2, n) : exp2f(l2 * (float)(n - R)));
   } else if (tid < 3 * C) {
     const int n = tid - 2 * C;
-    s_w[n] = P.alpha * lin_pow(l2, n);
-    s_c[P.reverse ? n : C - 1 - n] = P.alpha * lin_pow(l2, n);
+    s_w[n] = P.alpha * (two ? P.beta * lin_pow(l2, n) : exp2f(l2 * (float)(R - (P.reverse ? C - n : n + 1))));
+    s_c[P.reverse ? n : C - 1 - n] = P.alpha * frame * lin_pow(l2, n);
   }
   if (warp == 0) tmem_alloc(&s_tmem, (uint32_t)K::TCOLS);
   tc_fence_before();
@@ -358,7 +369,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
+    } else {
       // ------------------------------ products -----------------------------
       constexpr uint32_t id_p = umma_idesc_16(X::kType, C, C, false, false);
       constexpr uint32_t id_o1 = umma_idesc_16(X::kType, DC, C, false, false);
@@ -383,20 +394,11 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       using Mn = std::integral_constant<int, 0>;
       using DSteps = std::integral_constant<int, DA / 16>;
       using CSteps = std::integral_constant<int, C / 16>;
-      auto scores = [&](int m) {   // P of chunk m
-        if (elect_one()) {
-          product(tmem + K::COL_P, kmaj(sA(m % NS)), Box{}, kmaj(sB(m % NS)), Box{}, DSteps{}, id_p, false);
-          umma_commit(&bar_pacc);
-        }
-        __syncwarp();
-      };
-      bool ok = M > 0 && lin_wait(&bar_full[0], 0u, &s_abort);
-      tc_fence_after();
-      if (!STATE_ONLY && ok) scores(0);
-      for (int m = 0; m < M && ok; ++m) {
+      bool ok = true;
+      for (int m = 0; m < M && ok && warp == 1; ++m) {
         const int st = m % NS;
         // what the chunk adds to the state, once what the chunk before added is read
-        if (!(ok = lin_wait(&bar_cp, (unsigned)m & 1u, &s_abort))) break;
+        if (!(ok = lin_wait(&bar_cp[m & 1], (unsigned)(m >> 1) & 1u, &s_abort))) break;
         if (m > 0 && !(ok = lin_wait(&bar_ur, (unsigned)(m - 1) & 1u, &s_abort))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -406,38 +408,45 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
             if constexpr (K::TS) {
 #pragma unroll
               for (int k = 0; k < C / 16; ++k)
-                umma_16_ts(tmem + K::COL_U, tmem + K::COL_CP + 32 * p + 8 * k, db + (uint64_t)(k * 2048 >> 4), id_u_ts, (p || k) ? 1u : 0u);
+                umma_16_ts(tmem + K::COL_U, tmem + K::COL_CP + 32 * K::NP * (m & 1) + 32 * p + 8 * k, db + (uint64_t)(k * 2048 >> 4),
+                           id_u_ts, (p || k) ? 1u : 0u);
             } else {
-              product(tmem + K::COL_U, mnmaj(base + K::OFF_CP + p * K::C_BYTES), Mn{}, db, Mn{}, CSteps{}, id_u, p > 0);
+              product(tmem + K::COL_U, mnmaj(base + K::OFF_CP + (K::NP * (m & 1) + p) * K::C_BYTES), Mn{}, db, Mn{}, CSteps{}, id_u, p > 0);
             }
           }
           umma_commit(&bar_u);
-          if (STATE_ONLY) umma_commit(&bar_empty[st]);
+          umma_commit(&bar_cpf[m & 1]);
+          umma_commit(&bar_empty[st]);
         }
         __syncwarp();
-        // the state's share of the outputs
+      }
+      // the outputs: the state's share and the chunk's own, once what their columns held is read
+      for (int m = 0; m < M && ok && warp == 2 && !STATE_ONLY; ++m) {
+        const int st = m % NS, before = two ? m - 1 : m - 2;
+        if (!(ok = lin_wait(&bar_p[m & 1], (unsigned)(m >> 1) & 1u, &s_abort))) break;
+        if (before >= 0 && !(ok = lin_wait(&bar_o[before & 1], (unsigned)(before >> 1) & 1u, &s_abort))) break;
+        if (rows_of(m) < C && !(ok = lin_wait(&bar_zero, 0u, &s_abort))) break;
         if (!(ok = lin_wait(&bar_s, (unsigned)m & 1u, &s_abort))) break;
-        if (STATE_ONLY) {
-          if (m + 1 < M && !(ok = lin_wait(&bar_full[(m + 1) % NS], (unsigned)((m + 1) / NS) & 1u, &s_abort))) break;
-          continue;
-        }
         tc_fence_after();
         if (elect_one()) {
-          product(tmem + K::COL_O1 + (m & 1) * 64, d_sb, SBox{}, kmaj(sA(st)), Box{}, DSteps{}, id_o1, false);
+          const uint32_t o1 = tmem + K::COL_O + (two ? 0 : 64 * (m & 1)), o2 = tmem + K::COL_O + (two ? 64 : 64 * (m & 1));
+          product(o1, d_sb, SBox{}, kmaj(sA(st)), Box{}, DSteps{}, id_o1, false);
           umma_commit(&bar_o1);
+          product(o2, mnmaj(sC(st)), Mn{}, kmaj(base + K::OFF_P + (m & 1) * K::P_BYTES), Box{}, CSteps{}, id_o2, !two);
+          umma_commit(&bar_oacc[m & 1]);
+          umma_commit(&bar_empty[st]);
         }
         __syncwarp();
-        if (!(ok = lin_wait(&bar_p, (unsigned)m & 1u, &s_abort))) break;
-        if (m + 1 < M) {
-          if (!(ok = lin_wait(&bar_full[(m + 1) % NS], (unsigned)((m + 1) / NS) & 1u, &s_abort))) break;
-          tc_fence_after();
-          scores(m + 1);
-        }
-        if (m > 0 && !(ok = lin_wait(&bar_o, (unsigned)(m - 1) & 1u, &s_abort))) break;
+      }
+      // P, once the chunk before's is read
+      for (int m = 0; m < M && ok && warp == 3 && !STATE_ONLY; ++m) {
+        const int st = m % NS;
+        if (!(ok = lin_wait(&bar_full[st], (unsigned)(m / NS) & 1u, &s_abort))) break;
+        if (m > 0 && !(ok = lin_wait(&bar_p[(m - 1) & 1], (unsigned)((m - 1) >> 1) & 1u, &s_abort))) break;
         tc_fence_after();
         if (elect_one()) {
-          product(tmem + K::COL_O2, mnmaj(sC(st)), Mn{}, kmaj(base + K::OFF_P + (m & 1) * K::P_BYTES), Box{}, CSteps{}, id_o2, false);
-          umma_commit(&bar_oacc);
+          product(tmem + K::COL_P, kmaj(sA(st)), Box{}, kmaj(sB(st)), Box{}, DSteps{}, id_p, false);
+          umma_commit(&bar_pacc);
           umma_commit(&bar_empty[st]);
         }
         __syncwarp();
@@ -450,17 +459,18 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
       const int fr = lane >> 2, fc = 2 * (lane & 3);   // this thread's row and column of an 8 x 8 fragment
       const int mr = lane & 7, mi = lane >> 3;         // the row and matrix it addresses
-      // rows 16 w .. of P (an M = 64 accumulator takes lanes 0-15 of each quarter); alpha beta e^{g|i-j|} on one side of
-      // the diagonal, zero on the other
+      // rows 16 w .. of P (an M = 64 accumulator takes lanes 0-15 of each quarter); the weights on this side of the
+      // diagonal, zero on the other
       float wt[32];
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const int i = 16 * w + fr + (e & 2) * 4, jj = (e >> 2) * 8 + fc + (e & 1);
         const int n = P.reverse ? jj - i : i - jj;
-        wt[e] = n >= 0 ? P.beta * s_w[n >= 0 ? n : 0] : 0.0f;
+        wt[e] = n >= 0 ? s_w[two ? (n >= 0 ? n : 0) : jj] : 0.0f;
       }
       const int pi = 16 * w + mr + (mi & 1) * 8;       // row of P~ addressed; matrices: rows, rows + 8, next 8 columns
       for (int m = 0; m < M; ++m) {
+        if (m > 1 && !lin_wait(&bar_oacc[m & 1], (unsigned)((m >> 1) - 1) & 1u, &s_abort)) break;   // P~ two chunks ago is used
         if (!lin_wait(&bar_pacc, (unsigned)m & 1u, &s_abort)) break;
         tc_fence_after();
         const int n = rows_of(m);
@@ -485,7 +495,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
         fence_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_p);
+        if (lane == 0) mbar_arrive(&bar_p[m & 1]);
       }
     }
   } else if (warp < 12) {
@@ -498,7 +508,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       const bool wide = P.out_map || (((uintptr_t)P.out | (uintptr_t)(2 * P.out_bs) | (uintptr_t)(2 * P.out_ts) | (uintptr_t)(2 * P.out_hs)) & 15u) == 0;
       unsigned char* stage = base + K::OFF_O;
       for (int m = 0; m < M; ++m) {
-        const bool ok = lin_wait(&bar_oacc, (unsigned)m & 1u, &s_abort);
+        const bool ok = lin_wait(&bar_oacc[m & 1], (unsigned)(m >> 1) & 1u, &s_abort);
         if (t == 0) bulk_wait_read();   // the copy before has read the staged outputs
         if (!named_barrier_and(1, 128, ok)) break;   // one decision; and the staged outputs before these are gone
         tc_fence_after();
@@ -508,21 +518,25 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
 #pragma unroll 2
         for (int q = 0; q < DC / 32; ++q) {   // 16 columns of c and 32 rows at a time
           const int g = DC == 128 ? q >> 1 : 0, r0 = 32 * (DC == 128 ? q & 1 : q);
-          const uint32_t a = lanes + ((uint32_t)(16 * g) << 16) + (uint32_t)r0;
-          float x[16], y[16];
-          tmem_frag16(a + (uint32_t)(K::COL_O1 + (m & 1) * 64), x);
-          tmem_frag16(a + (uint32_t)K::COL_O2, y);
+          const uint32_t a = lanes + ((uint32_t)(16 * g) << 16) + (uint32_t)(K::COL_O + r0);
+          float x[16];
+          tmem_frag16(two ? a : a + (uint32_t)(64 * (m & 1)), x);
           tmem_wait16(x);
-          tmem_wait16(y);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 f2 = *reinterpret_cast<const float2*>(f + r0 + 8 * k);
-            const unsigned long long ff = pack2(f2.x, f2.y);
+            const unsigned long long ff = *reinterpret_cast<const unsigned long long*>(f + r0 + 8 * k);
 #pragma unroll
-            for (int e = 4 * k; e < 4 * k + 4; e += 2) unpack2(fma2(ff, pack2(x[e], x[e + 1]), pack2(y[e], y[e + 1])), x[e], x[e + 1]);
+            for (int e = 4 * k; e < 4 * k + 4; e += 2) unpack2(mul2(ff, pack2(x[e], x[e + 1])), x[e], x[e + 1]);
+          }
+          if (two) {
+            float y[16];
+            tmem_frag16(a + 64u, y);
+            tmem_wait16(y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] += y[e];
           }
           const int c0 = DC == 128 ? 32 * w + 16 * g : 16 * w;   // first column of c
-          if (P.out_f32) {
+          if constexpr (WHAT == kLinOutF32) {
             float* o = (float*)P.out + at + (start + (long long)chunk_of(m) * C) * P.out_ts + c0 + fr;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -541,8 +555,8 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
         }
         tc_fence_before();   // the accumulators are read
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_o);
-        if (!P.out_f32 && n == C && P.out_map) {
+        if (lane == 0) mbar_arrive(&bar_o[m & 1]);
+        if (WHAT == kLinOut && n == C && P.out_map) {
           fence_async_smem();
           named_barrier(1, 128);
           if (t == 0) {
@@ -551,7 +565,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
               if (dc0 + 64 * x < P.dc) tma_store_4d(&maps.o, dc0 + 64 * x, h, (int)start + chunk_of(m) * C, P.cu ? 0 : s, stage + x * K::SUB);
             bulk_commit();
           }
-        } else if (!P.out_f32) {
+        } else if (WHAT == kLinOut) {
           named_barrier(1, 128);
           // 16 bytes a thread, a row's neighbours side by side
 #pragma unroll 1
@@ -609,6 +623,11 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     // element e of block (b, q): column c_of(b, e) of c, column d_of(q, e) of a and b
     auto c_of = [&](int b, int e) { return (DC == 128 ? 32 * w + 16 * b : 16 * w) + fr + (e & 2) * 4; };
     auto d_of = [&](int q, int e) { return half + 32 * q + (e >> 2) * 8 + fc + (e & 1); };
+    // Against time the first chunk's rows (a short chunk, or the last row undecayed) see the state this much earlier than
+    // those of a whole one, for which the row factors and P~ are made: it enters that much larger, and decays as over a
+    // whole chunk.
+    const int early = P.reverse && !two && M > 0 && !STATE_ONLY ? C - rows_of(0) + e0 : 0;
+    const float lead = frame * exp2f(-l2 * (float)early);
     float S[NB][NQ][16];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -617,28 +636,37 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int c = dc0 + c_of(b, e), d = d_of(q, e);
-          S[b][q][e] = (src && c < P.dc && d < P.da) ? src[d * sd + c * sj] : 0.0f;
+          S[b][q][e] = (src && c < P.dc && d < P.da) ? lead * src[d * sd + c * sj] : 0.0f;
         }
+    if (!two) f_out *= exp2f(-l2 * R);
+    if (STATE_ONLY) f_out = 1.0f;
     const float f_full = lin_pow(l2, C);
     bool ok = true;
     for (int m = 0; m <= M; ++m) {
       if (m > 0) {
         if (!(ok = lin_wait(&bar_u, (unsigned)(m - 1) & 1u, &s_abort))) break;
         tc_fence_after();
-        const int n = rows_of(m - 1) - (m == 1 ? e0 : 0);
+        const int n = rows_of(m - 1) - (m == 1 ? e0 - early : 0);
         const float f = n == C ? f_full : lin_pow(l2, n);
         const unsigned long long ff = pack2(f, f);
+        auto add = [&](float (&v)[16], const float (&u)[16]) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+          for (int e = 0; e < 16; e += 2) unpack2(fma2(ff, pack2(v[e], v[e + 1]), pack2(u[e], u[e + 1])), v[e], v[e + 1]);
+        };
+        auto where = [&](int b, int q) { return lanes + ((uint32_t)(16 * b) << 16) + (uint32_t)(K::COL_U + half + 32 * q); };
+        constexpr int NX = NB * NQ;
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            float u[16];
-            tmem_frag16(lanes + ((uint32_t)(16 * b) << 16) + (uint32_t)(K::COL_U + half + 32 * q), u);
-            tmem_wait16(u);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              unpack2(fma2(ff, pack2(S[b][q][e], S[b][q][e + 1]), pack2(u[e], u[e + 1])), S[b][q][e], S[b][q][e + 1]);
+        for (int x = 0; x < NX; x += 2) {   // two blocks in flight
+          float u[16], u2[16];
+          tmem_frag16(where(x / NQ, x % NQ), u);
+          if (x + 1 < NX) tmem_frag16(where((x + 1) / NQ, (x + 1) % NQ), u2);
+          tmem_wait16(u);
+          add(S[x / NQ][x % NQ], u);
+          if (x + 1 < NX) {
+            tmem_wait16(u2);
+            add(S[(x + 1) / NQ][(x + 1) % NQ], u2);
           }
+        }
         tc_fence_before();   // U is read
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_ur);
@@ -703,8 +731,11 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
             for (int x = 0; x < DA / 64; ++x) *reinterpret_cast<uint4*>(sB(st) + x * K::SUB + (t + 256 * k) * 16) = z;
           }
         }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_zero);
       }
-      if (m > 0 && !lin_wait(&bar_u, (unsigned)(m - 1) & 1u, &s_abort)) break;   // the pieces are free
+      if (m > 1 && !lin_wait(&bar_cpf[m & 1], (unsigned)((m >> 1) - 1) & 1u, &s_abort)) break;   // the pieces two chunks ago are used
       if constexpr (K::TS) {
         __syncwarp();
 #pragma unroll 1
@@ -727,7 +758,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
             for (int i = 2 * k; i < 2 * k + 2; ++i) X::pieces(wt, v[i], o[0][i], o[1][i], o[2][i]);
           }
 #pragma unroll
-          for (int p = 0; p < 3; ++p) tmem_st_frag4(to_tmem + (uint32_t)(32 * p + 8 * jb), o[p]);
+          for (int p = 0; p < 3; ++p) tmem_st_frag4(to_tmem + (uint32_t)(32 * K::NP * (m & 1) + 32 * p + 8 * jb), o[p]);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -743,7 +774,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
             uint32_t o[3][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) X::pieces(pack2(wk, wk), cu[i], o[0][i], o[1][i], o[2][i]);
-            unsigned char* to = base + K::OFF_CP + x * K::SUB + (t + 256 * k) * 16;
+            unsigned char* to = base + K::OFF_CP + K::NP * (m & 1) * K::C_BYTES + x * K::SUB + (t + 256 * k) * 16;
 #pragma unroll
             for (int p = 0; p < 3; ++p)
               *reinterpret_cast<uint4*>(to + p * K::C_BYTES) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
@@ -752,7 +783,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_cp);
+      if (lane == 0) mbar_arrive(&bar_cp[m & 1]);
     }
   }
 
@@ -762,9 +793,9 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     const int n = s_loaded;
     for (int m = n > NS ? n - NS : 0; m < n; ++m) mbar_drain(&bar_full[m % NS], (unsigned)(m / NS) & 1u, kLinWaitNs);
   }
-  if (warp == 1) {
-    if (elect_one()) umma_commit(&bar_done);
-    mbar_drain(&bar_done, 0u, kLinWaitNs);
+  if (warp >= 1 && warp <= 3) {
+    if (elect_one()) umma_commit(&bar_done[warp - 1]);
+    mbar_drain(&bar_done[warp - 1], 0u, kLinWaitNs);
   }
   tc_fence_before();
   __syncthreads();
