@@ -231,6 +231,8 @@ struct LinMaps {
   CUtensorMap a, b, c, o;
 };
 
+constexpr int kLinSorted = 512;   // up to this many sequences are taken by length (each CTA ranks them: n^2 / 896 steps a thread)
+
 template <int DA, int DC>
 struct LinTcCfg {
   static constexpr int C = 64;
@@ -279,7 +281,26 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
   __shared__ __align__(16) float s_c[C];        // the weights of c', from the far end of a whole chunk
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int sh = blockIdx.y, h = sh % P.H, s = sh / P.H;
+  // CTAs start in the order of their numbers, each for the whole of its part: the longest sequences first, so that no long
+  // one starts late (16 sequences of 0 .. 4000 rows: 387 -> 290 us)
+  const int h = blockIdx.y % P.H;
+  int s = blockIdx.y / P.H;
+  if (P.cu && P.n_seq > 1 && P.n_seq <= kLinSorted) {
+    __shared__ int s_seq;
+    for (int i = threadIdx.x; i < P.n_seq; i += K::NT) {
+      long long at;
+      int li, lj, rank = 0;
+      lin_rows(P, i, at, li);
+      for (int j = 0; j < P.n_seq; ++j) {
+        lin_rows(P, j, at, lj);
+        rank += lj > li || (lj == li && j < i);
+      }
+      if (rank == s) s_seq = i;
+    }
+    __syncthreads();
+    s = s_seq;
+  }
+  const int sh = s * P.H + h;
   const int dc0 = blockIdx.x * DC;
   const int part = blockIdx.z;
   const float l2 = G.log2[h];
