@@ -16,12 +16,29 @@ from typing import Optional
 
 import numpy as np
 
-from ._binding import (PN_BF16, PN_F16, PN_F32, PN_OK, PN_ROT_HALF, PN_ROT_INTERLEAVED, PN_ROT_LINEAR, PN_ROT_NTK,
-                       PN_ROT_PLAIN, PN_ROT_YARN, PnError, lib, pn_heads, pn_last_error, pn_rotary_desc)
+from ._binding import (LIB_PATH, PN_BF16, PN_F16, PN_F32, PN_OK, PN_ROT_HALF, PN_ROT_INTERLEAVED, PN_ROT_LINEAR, PN_ROT_NTK,
+                       PN_ROT_PLAIN, PN_ROT_YARN, PnError, SIGNATURES, lib, pn_heads, pn_last_error,
+                       pn_rotary_desc)
 
 _LAYOUTS = {"half": PN_ROT_HALF, "interleaved": PN_ROT_INTERLEAVED}
 _SCALINGS = {"none": PN_ROT_PLAIN, "linear": PN_ROT_LINEAR, "ntk": PN_ROT_NTK, "yarn": PN_ROT_YARN}
 _DTYPES = None
+_HEADS_BYTES = ctypes.sizeof(pn_heads)
+
+
+def _addresses() -> ctypes.CDLL:
+    """The library again with every pointer as a plain address: the pn_heads of one call are rows of one array."""
+    fast = ctypes.CDLL(LIB_PATH)
+    for name in ("pn_rotary_apply", "pn_norm_rotary_apply", "pn_norm_rotary_backward", "pn_linattn_forward",
+                 "pn_linattn_backward", "pn_linattn_step"):
+        res, args = SIGNATURES[name]
+        fn = getattr(fast, name)
+        fn.restype, fn.argtypes = res, [ctypes.c_void_p if issubclass(a, ctypes._Pointer) else a for a in args]
+    return fast
+
+
+fast = _addresses()
+_ROWS = {n: ctypes.c_longlong * (4 * n) for n in (4, 6, 7)}
 
 
 def _dtypes():
@@ -44,39 +61,49 @@ def _ok(status: int) -> None:
         raise PnError(status, pn_last_error(None))
 
 
-def _same(name, t, like):
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {t.dtype} on {t.device}; {like.dtype} on {like.device} is wanted")
-
-
-def _heads(name, t, like, lead=None, heads=None, dim=None):
-    """pn_heads of a [tokens, heads, dim] or [batch, tokens, heads, dim] tensor."""
-    if t.dim() not in (3, 4):
+def _first(name, t):
+    """Checks of the tensor that the others are held to: its leading sizes."""
+    shape = t.shape
+    if len(shape) not in (3, 4):
         raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    _same(name, t, like)
-    shape = t.shape
-    if (lead is not None and tuple(shape[:-2]) != tuple(lead)) or (heads is not None and shape[-2] != heads) \
-            or (dim is not None and shape[-1] != dim):
-        raise ValueError(f"{name} has shape {tuple(shape)}; {(*(lead or ('..',)), heads, dim)} is wanted")
+    return shape[:-2]
+
+
+def _heads(name, t, like, shape):
+    """(address, batch, token and head stride) of a tensor of that shape, type and device."""
+    if t.shape != shape or t.dtype is not like.dtype or t.device != like.device:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}; {tuple(shape)} {like.dtype} on {like.device} "
+                         "is wanted")
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1 and t.numel():
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
-    if t.dim() == 3:
-        return pn_heads(t.data_ptr(), 0, st[0], st[1])
-    return pn_heads(t.data_ptr(), st[0], st[1], st[2])
+    if len(st) == 3:
+        return t.data_ptr(), 0, st[0], st[1]
+    return t.data_ptr(), st[0], st[1], st[2]
 
 
-def _distinct(name, t):
-    """Outputs whose elements share memory (expanded tensors) are refused."""
-    for n, s in zip(t.shape, t.stride()):
-        if n > 1 and s == 0:
-            raise ValueError(f"{name} has overlapping elements")
+def _output(name, t, like, shape):
+    """The same of an output: tensors whose elements share memory (expanded ones) are refused."""
+    h = _heads(name, t, like, shape)
+    if 0 in h[1:]:
+        for n, s in zip(t.shape, t.stride()):
+            if n > 1 and s == 0:
+                raise ValueError(f"{name} has overlapping elements")
+    return h
+
+
+def _rows(*heads):
+    """One array of all of them, and the address of each."""
+    flat = [v for h in heads for v in h]
+    array = _ROWS[len(heads)](*flat)
+    at = ctypes.addressof(array)
+    return array, [at + _HEADS_BYTES * i for i in range(len(heads))]
 
 
 def _ints(name, t, shape, dtype, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
@@ -85,7 +112,7 @@ def _float32(name, t, shape, device):
     import torch
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on {device}")
     return t.data_ptr()
 
@@ -93,14 +120,17 @@ def _float32(name, t, shape, device):
 def _weights(wq, wk, dim, like):
     """Pointers and type of a norm's weights: float32, or the queries' type."""
     for name, w in (("wq", wq), ("wk", wk)):
-        if tuple(w.shape) != (dim,) or not w.is_contiguous() or w.device != like.device or w.dtype != wq.dtype:
+        if w.shape != (dim,) or not w.is_contiguous() or w.device != like.device or w.dtype is not wq.dtype:
             raise ValueError(f"{name} must be a contiguous [{dim}] tensor on {like.device}, both weights of one type")
     return wq.data_ptr(), wk.data_ptr(), _dtype("wq", wq)
 
 
 def _stream(device):
     import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    try:   # torch.cuda.current_stream without its Stream object
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _workspace(n, device):
@@ -141,34 +171,39 @@ class Rotary:
         self.h = h.value
 
     def __del__(self):
-        if getattr(self, "h", None):
-            lib.pn_rotary_destroy(self.h)
-            self.h = None
+        try:
+            if self.h:
+                lib.pn_rotary_destroy(self.h)
+                self.h = None
+        except Exception:   # the interpreter is going down
+            pass
 
     @staticmethod
-    def _shape(q, k):
-        hq = _heads("q", q, q)
-        hk = _heads("k", k, q, lead=q.shape[:-2], dim=q.shape[-1])
-        B, T = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
-        return hq, hk, (_dtype("q", q), B, T, q.shape[-2], k.shape[-2], q.shape[-1])
+    def _operands(q, k):
+        """(rows of q, rows of k, k's shape, (dtype, B, T, Hq, Hk, dim))."""
+        lead = _first("q", q)
+        sq, sk = q.shape, k.shape
+        want = lead + (sk[-2] if len(sk) > 1 else 0, sq[-1])
+        B, T = (1, sq[0]) if len(lead) == 1 else lead
+        return _heads("q", q, q, sq), _heads("k", k, q, want), want, (_dtype("q", q), B, T, sq[-2], want[-2], sq[-1])
 
-    def _out(self, q, k, out):
+    @staticmethod
+    def _out(q, k, sk, out):
         import torch
         if out is None:
-            out = (torch.empty(q.shape, dtype=q.dtype, device=q.device), torch.empty(k.shape, dtype=k.dtype, device=k.device))
+            oq, ok = torch.empty_like(q), torch.empty_like(k)
+            return (oq, ok), _heads("q", oq, q, q.shape), _heads("k", ok, q, sk)
         oq, ok = out
-        hq = _heads("out[0]", oq, q, q.shape[:-2], q.shape[-2], q.shape[-1])
-        hk = _heads("out[1]", ok, q, k.shape[:-2], k.shape[-2], k.shape[-1])
-        _distinct("out[0]", oq)
-        _distinct("out[1]", ok)
-        return out, hq, hk
+        return (oq, ok), _output("out[0]", oq, q, q.shape), _output("out[1]", ok, q, sk)
 
     def _rotate(self, q, k, positions, out, inverse):
         import torch
-        hq, hk, shape = self._shape(q, k)
-        pos = _ints("positions", positions, q.shape[:-2], torch.int64, q.device)
-        out, oq, ok = self._out(q, k, out)
-        _ok(lib.pn_rotary_apply(self.h, *shape, hq, hk, pos, inverse, oq, ok, _stream(q.device)))
+        hq, hk, sk, shape = self._operands(q, k)
+        device = q.device
+        pos = _ints("positions", positions, q.shape[:-2], torch.int64, device)
+        out, oq, ok = self._out(q, k, sk, out)
+        keep, at = _rows(hq, hk, oq, ok)
+        _ok(fast.pn_rotary_apply(self.h, *shape, at[0], at[1], pos, inverse, at[2], at[3], _stream(device)))
         return out
 
     def apply(self, q, k, positions, out=None):
@@ -184,26 +219,31 @@ class Rotary:
         """x_j w_j / sqrt(mean(x^2) + eps) of each head vector, then the rotation, in one pass.  The weights are [dim],
         float32 or of the queries' type."""
         import torch
-        hq, hk, shape = self._shape(q, k)
-        pos = _ints("positions", positions, q.shape[:-2], torch.int64, q.device)
-        out, oq, ok = self._out(q, k, out)
-        _ok(lib.pn_norm_rotary_apply(self.h, *shape, hq, hk, pos, *_weights(wq, wk, q.shape[-1], q), eps, oq, ok,
-                                     _stream(q.device)))
+        hq, hk, sk, shape = self._operands(q, k)
+        device = q.device
+        pos = _ints("positions", positions, q.shape[:-2], torch.int64, device)
+        w = _weights(wq, wk, shape[-1], q)
+        out, oq, ok = self._out(q, k, sk, out)
+        keep, at = _rows(hq, hk, oq, ok)
+        _ok(fast.pn_norm_rotary_apply(self.h, *shape, at[0], at[1], pos, *w, eps, at[2], at[3], _stream(device)))
         return out
 
     def norm_backward(self, dq_out, dk_out, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
         """(dq, dk, dwq, dwk) of :meth:`norm_apply`; dwq and dwk are float32 [dim].  ``out`` may be (dq_out, dk_out)."""
         import torch
-        hq, hk, shape = self._shape(q, k)
-        gq = _heads("dq_out", dq_out, q, q.shape[:-2], q.shape[-2], q.shape[-1])
-        gk = _heads("dk_out", dk_out, q, k.shape[:-2], k.shape[-2], k.shape[-1])
-        pos = _ints("positions", positions, q.shape[:-2], torch.int64, q.device)
-        out, oq, ok = self._out(q, k, out)
-        dw = torch.empty(2, q.shape[-1], dtype=torch.float32, device=q.device)
+        hq, hk, sk, shape = self._operands(q, k)
+        device = q.device
+        gq, gk = _heads("dq_out", dq_out, q, q.shape), _heads("dk_out", dk_out, q, sk)
+        pos = _ints("positions", positions, q.shape[:-2], torch.int64, device)
+        w = _weights(wq, wk, shape[-1], q)
+        out, oq, ok = self._out(q, k, sk, out)
+        dw = torch.empty(2, shape[-1], dtype=torch.float32, device=device)
         n = lib.pn_norm_rotary_workspace(*shape[1:])
-        keep, ws = _workspace(n, q.device)
-        _ok(lib.pn_norm_rotary_backward(self.h, *shape, gq, gk, hq, hk, pos, *_weights(wq, wk, q.shape[-1], q), eps, oq,
-                                        ok, dw[0].data_ptr(), dw[1].data_ptr(), ws, n, _stream(q.device)))
+        keep_w, ws = _workspace(n, device)
+        keep, at = _rows(gq, gk, hq, hk, oq, ok)
+        at_w = dw.data_ptr()
+        _ok(fast.pn_norm_rotary_backward(self.h, *shape, *at[:4], pos, *w, eps, at[4], at[5], at_w, at_w + 4 * shape[-1], ws,
+                                         n, _stream(device)))
         return out[0], out[1], dw[0], dw[1]
 
 
@@ -238,16 +278,20 @@ class LinearAttention:
         self.h = h.value
 
     def __del__(self):
-        if getattr(self, "h", None):
-            lib.pn_linattn_destroy(self.h)
-            self.h = None
+        try:
+            if self.h:
+                lib.pn_linattn_destroy(self.h)
+                self.h = None
+        except Exception:   # the interpreter is going down
+            pass
 
     def _operands(self, q, k, v):
-        if q.dtype != self.dtype:
+        """Rows of q, k and v, and the shape of the outputs."""
+        lead = _first("q", q)
+        if q.dtype is not self.dtype:
             raise ValueError(f"q is {q.dtype}; {self.dtype} is wanted")
-        lead = q.shape[:-2]
-        return (_heads("q", q, q, lead, self.heads, self.dk), _heads("k", k, q, lead, self.kv_heads, self.dk),
-                _heads("v", v, q, lead, self.kv_heads, self.dv))
+        return (_heads("q", q, q, lead + (self.heads, self.dk)), _heads("k", k, q, lead + (self.kv_heads, self.dk)),
+                _heads("v", v, q, lead + (self.kv_heads, self.dv)), lead + (self.heads, self.dv))
 
     def _sequences(self, q, cu_seqlens, max_len):
         """(n_seq, T, cu pointer, max_len) of the rows."""
@@ -270,19 +314,18 @@ class LinearAttention:
         written.  ``max_len``: the longest sequence, a hint for the work's split.  States: float32
         [sequences, heads, dk, dv].  ``out``: a tensor for o."""
         import torch
-        hq, hk, hv = self._operands(q, k, v)
+        hq, hk, hv, so = self._operands(q, k, v)
         n, T, cu, max_len = self._sequences(q, cu_seqlens, max_len)
-        shape = (n, self.heads, self.dk, self.dv)
-        s0 = _float32("initial_state", initial_state, shape, q.device)
-        state = torch.empty(shape, dtype=torch.float32, device=q.device)
+        shape, device = (n, self.heads, self.dk, self.dv), q.device
+        s0 = _float32("initial_state", initial_state, shape, device)
+        state = torch.empty(shape, dtype=torch.float32, device=device)
         if out is None:
-            out = torch.empty(*q.shape[:-1], self.dv, dtype=q.dtype, device=q.device)
-        ho = _heads("out", out, q, q.shape[:-2], self.heads, self.dv)
-        _distinct("out", out)
+            out = torch.empty(so, dtype=q.dtype, device=device)
+        ho = _output("out", out, q, so)
         size = lib.pn_linattn_workspace(self.h, 0, n, T, cu is not None, max_len)
-        keep, ws = _workspace(size, q.device)
-        _ok(lib.pn_linattn_forward(self.h, n, T, cu, max_len, hq, hk, hv, s0, ho, state.data_ptr(), ws, size,
-                                   _stream(q.device)))
+        keep_w, ws = _workspace(size, device)
+        keep, at = _rows(hq, hk, hv, ho)
+        _ok(fast.pn_linattn_forward(self.h, n, T, cu, max_len, *at[:3], s0, at[3], state.data_ptr(), ws, size, _stream(device)))
         return out, state
 
     def backward(self, do, q, k, v, initial_state=None, dstate=None, cu_seqlens=None, max_len: Optional[int] = None,
@@ -290,25 +333,22 @@ class LinearAttention:
         """(dq, dk, dv, gradient of the initial state) of :meth:`forward` with the same inputs, from the gradients of o
         and (None: zero) of the final state.  ``grads``: a triple of tensors for dq, dk and dv."""
         import torch
-        hq, hk, hv = self._operands(q, k, v)
+        hq, hk, hv, so = self._operands(q, k, v)
         n, T, cu, max_len = self._sequences(q, cu_seqlens, max_len)
-        shape = (n, self.heads, self.dk, self.dv)
-        hdo = _heads("do", do, q, q.shape[:-2], self.heads, self.dv)
-        s0 = _float32("initial_state", initial_state, shape, q.device)
-        ds = _float32("dstate", dstate, shape, q.device)
+        shape, device = (n, self.heads, self.dk, self.dv), q.device
+        hdo = _heads("do", do, q, so)
+        s0 = _float32("initial_state", initial_state, shape, device)
+        ds = _float32("dstate", dstate, shape, device)
         if grads is None:
-            grads = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
-        dq, dk, dv = grads
-        outs = []
-        for name, t, like in (("grads[0]", dq, q), ("grads[1]", dk, k), ("grads[2]", dv, v)):
-            outs.append(_heads(name, t, q, like.shape[:-2], like.shape[-2], like.shape[-1]))
-            _distinct(name, t)
-        ds0 = torch.empty(shape, dtype=torch.float32, device=q.device)
+            grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+        outs = [_output(f"grads[{i}]", g, q, x.shape) for i, (g, x) in enumerate(zip(grads, (q, k, v)))]
+        ds0 = torch.empty(shape, dtype=torch.float32, device=device)
         size = lib.pn_linattn_workspace(self.h, 1, n, T, cu is not None, max_len)
-        keep, ws = _workspace(size, q.device)
-        _ok(lib.pn_linattn_backward(self.h, n, T, cu, max_len, hdo, hq, hk, hv, s0, ds, *outs, ds0.data_ptr(), ws, size,
-                                    _stream(q.device)))
-        return dq, dk, dv, ds0
+        keep_w, ws = _workspace(size, device)
+        keep, at = _rows(hdo, hq, hk, hv, *outs)
+        _ok(fast.pn_linattn_backward(self.h, n, T, cu, max_len, *at[:4], s0, ds, *at[4:], ds0.data_ptr(), ws, size,
+                                     _stream(device)))
+        return (*grads, ds0)
 
     @staticmethod
     def check(device=None):
@@ -329,24 +369,25 @@ class LinearAttention:
         import torch
         if q.dim() != 3:
             raise ValueError("q must be [rows, heads, dk]")
-        ops = self._operands(q, k, v)
+        hq, hk, hv, so = self._operands(q, k, v)
+        rows, device = so[0], q.device
         if out is None:
-            out = torch.empty(q.shape[0], self.heads, self.dv, dtype=q.dtype, device=q.device)
-        ops += (_heads("out", out, q, q.shape[:-2], self.heads, self.dv),)
-        _distinct("out", out)
+            out = torch.empty(so, dtype=q.dtype, device=device)
+        ho = _output("out", out, q, so)
         if states.dim() != 4:
             raise ValueError("states must be [slots, heads, dk, dv]")
         n = states.shape[0]
-        st = _float32("states", states, (n, self.heads, self.dk, self.dv), q.device)
-        sl = None if slots is None else _ints("slots", slots, (q.shape[0],), torch.int64, q.device)
+        st = _float32("states", states, (n, self.heads, self.dk, self.dv), device)
+        sl = None if slots is None else _ints("slots", slots, (rows,), torch.int64, device)
         if (wq is None) != (wk is None):
             raise ValueError("wq and wk come together")
         w = (None, None, PN_F32) if wq is None else _weights(wq, wk, self.dk, q)
         if (rotary is None) != (positions is None):
             raise ValueError("rotary and positions come together")
-        pos = None if rotary is None else _ints("positions", positions, (q.shape[0],), torch.int64, q.device)
-        for x in ops:   # rows lie at the batch stride
-            x.batch_stride = x.token_stride
-        _ok(lib.pn_linattn_step(self.h, q.shape[0], *ops, st, n, sl, rotary.h if rotary is not None else None, pos, *w,
-                                eps, _stream(q.device)))
+        turn, pos = None, None
+        if rotary is not None:
+            turn, pos = rotary.h, _ints("positions", positions, (rows,), torch.int64, device)
+        # rows lie at the batch stride
+        keep, at = _rows(*[(h[0], h[2], 0, h[3]) for h in (hq, hk, hv, ho)])
+        _ok(fast.pn_linattn_step(self.h, rows, *at, st, n, sl, turn, pos, *w, eps, _stream(device)))
         return out
