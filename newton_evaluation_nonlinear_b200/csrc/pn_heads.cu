@@ -9,11 +9,15 @@
 //
 // All of it is bound by memory: each vector is read once and written once.  A
 // head vector is cut into units of two VE-element pieces, the two that hold a
-// rotation's pairs (piece u of the first half and of the second, or two
-// neighbours for the interleaved layout), so that every pair sits in one thread;
+// rotation's pairs (piece u of the first half and of the second; the interleaved
+// layout's pairs lie inside a piece, so there any two do, and they are taken so that a
+// group reads whole lines at once), so that every pair sits in one thread;
 // a group of lanes (the next power of two) takes one vector.  Angles depend on
 // (token, pair) alone, so a group takes several heads of one token with the same
-// sines.
+// sines.  What it takes to fill the memory is bytes in flight, and registers hold
+// too few of them next to sines, weights and sums: each thread copies its pieces of
+// the next vectors to slots of its own in shared memory (cp.async), several vectors
+// ahead, over the borders of tokens too, and needs no barrier to read them.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -56,7 +60,7 @@ struct HeadsArgs {
   int tokens;            // T of one batch entry
   long long rows;        // B * T
   int heads[2];          // query and key heads
-  int blocks[2];         // head blocks of hb heads per token
+  int blocks[2];         // blocks of hb heads per token
   int hb;
   int dim, rot;
   int half_units;        // units that hold rotated pairs of the half layout (0: interleaved)
@@ -65,6 +69,8 @@ struct HeadsArgs {
   float sign;            // +1, or -1 for the inverse rotation
   float m;
   float eps;
+  float inv_dim;
+  int items_fit;         // the list's numbers fit 31 bits
   int w_f32;             // weights are float32 (else the tensors' type)
   const long long* positions;
   const void* w[2];
@@ -79,13 +85,63 @@ struct HeadsArgs {
 
 constexpr int kHeadThreads = 256;
 
+constexpr int ahead(bool grad) { return grad ? 3 : 5; }   // slots: vectors on their way, and the one at hand
+
+template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+
+// One (token, block of heads) of a group's list.
+struct HeadsItem {
+  int kind, h0, h1;
+  long long b, t;
+  __device__ __forceinline__ void at(const HeadsArgs& A, long long it, int kind0, int per_token, bool grad) {
+    // (32-bit divisions where they reach: 64-bit ones take a hundred instructions)
+    int blk;
+    if (A.items_fit) {
+      const unsigned r = (unsigned)it / (unsigned)per_token;
+      blk = (int)((unsigned)it - r * (unsigned)per_token);
+      const unsigned bb = r / (unsigned)A.tokens;
+      b = bb;
+      t = r - bb * (unsigned)A.tokens;
+    } else {
+      const long long row = it / per_token;
+      blk = (int)(it - row * per_token);
+      b = row / A.tokens;
+      t = row - b * A.tokens;
+    }
+    kind = kind0;
+    if (!grad && blk >= A.blocks[0]) {
+      kind = 1;
+      blk -= A.blocks[0];
+    }
+    h0 = blk * A.hb;
+    h1 = min(A.heads[kind], h0 + A.hb);
+  }
+};
+
 // NU units per lane (1 for VE >= 4, where 32 lanes hold the widest vector)
 template <typename T, int VE, int NU, bool NORM, bool GRAD>
-__global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_constant__ HeadsArgs A, int group) {
+__global__ void __launch_bounds__(kHeadThreads, VE < 4 ? 1 : GRAD ? 2 : 3) heads_kernel(const __grid_constant__ HeadsArgs A, int group) {
+  constexpr bool kAsync = VE >= 4;            // (single elements are read straight)
+  constexpr int kSlots = kAsync ? ahead(GRAD) : 1;
+  constexpr int kPieces = GRAD ? 4 : 2;       // of one vector, or of it and its gradient
+  using Piece = typename RawVec<VE * (int)sizeof(T)>::type;
   __shared__ unsigned long long s_turn[kMaxRotPairs];
-  extern __shared__ float s_dw[];   // GRAD: [kHeadThreads / group][dim]
+  __shared__ __align__(16) float s_w[NORM ? 512 : 4];   // both weights
+  extern __shared__ __align__(16) unsigned char s_heads[];
+  Piece* slots = reinterpret_cast<Piece*>(s_heads) + threadIdx.x;   // piece p of slot s at (s * kPieces + p) * kHeadThreads
+  float* s_dw = reinterpret_cast<float*>(s_heads);                  // GRAD, at the end: [kHeadThreads / group][dim]
   const int pairs = A.rot >> 1;
   for (int i = threadIdx.x; i < pairs; i += kHeadThreads) s_turn[i] = A.turn[i];
+  if constexpr (NORM) {
+    for (int i = threadIdx.x; i < 2 * A.dim; i += kHeadThreads) {
+      const int kind = i >= A.dim, j = i - kind * A.dim;
+      s_w[i] = A.w_f32 ? ((const float*)A.w[kind])[j] : to_f<T>(((const T*)A.w[kind])[j]);
+    }
+  }
   __syncthreads();
 
   const int lane = threadIdx.x & (group - 1);
@@ -102,9 +158,12 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
     if (u < A.half_units) {
       c0[n] = u * VE;
       c1[n] = c0[n] + A.half_units * VE;
-    } else {
-      c0[n] = 2 * A.half_units * VE + 2 * (u - A.half_units) * VE;
-      c1[n] = c0[n] + VE;
+    } else if (VE == 1) {   // (an interleaved pair)
+      c0[n] = 2 * u;
+      c1[n] = c0[n] + 1;
+    } else {                // whole lines to a load, as above
+      c0[n] = (A.half_units + u) * VE;
+      c1[n] = c0[n] + (A.units - A.half_units) * VE;
     }
     on0[n] = u < A.units && c0[n] < A.dim;
     on1[n] = u < A.units && c1[n] < A.dim;
@@ -112,31 +171,65 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
 
   // items: (token, block of hb heads); the gradient's CTAs take queries only or keys only
   const int kind0 = GRAD ? ((int)blockIdx.x >= A.grid_q ? 1 : 0) : 0;
-  const long long per_token = GRAD ? A.blocks[kind0] : A.blocks[0] + A.blocks[1];
+  const int per_token = GRAD ? A.blocks[kind0] : A.blocks[0] + A.blocks[1];
   const long long items = A.rows * per_token;
   const long long first = (long long)(GRAD && kind0 ? blockIdx.x - A.grid_q : blockIdx.x) * per_cta + sub;
   const long long stride = (long long)(GRAD ? (kind0 ? gridDim.x - A.grid_q : A.grid_q) : gridDim.x) * per_cta;
 
-  float dw[GRAD ? 2 * NU * VE : 1];
-  if constexpr (GRAD) {
-#pragma unroll
-    for (int i = 0; i < 2 * NU * VE; ++i) dw[i] = 0.0f;
+  float dw[GRAD ? 2 * NU : 1][VE] = {};
+
+  // the vectors on their way
+  HeadsItem next;
+  long long next_it = first;
+  int next_h = 0;
+  const T *next_x = nullptr, *next_g = nullptr;
+  auto open = [&]() {
+    next.at(A, next_it, kind0, per_token, GRAD);
+    next_h = next.h0;
+    next_x = (const T*)A.x[next.kind] + next.b * A.xs[next.kind][0] + next.t * A.xs[next.kind][1] + next_h * A.xs[next.kind][2];
+    if constexpr (GRAD) next_g = (const T*)A.g[next.kind] + next.b * A.gs[next.kind][0] + next.t * A.gs[next.kind][1] + next_h * A.gs[next.kind][2];
+  };
+  auto fetch = [&](int slot) {
+    if constexpr (kAsync) {
+      if (next_it < items) {
+        Piece* to = slots + slot * (kPieces * kHeadThreads);
+        if (on0[0]) copy_async<sizeof(Piece)>(to, next_x + c0[0]);
+        if (on1[0]) copy_async<sizeof(Piece)>(to + kHeadThreads, next_x + c1[0]);
+        next_x += A.xs[next.kind][2];
+        if constexpr (GRAD) {
+          if (on0[0]) copy_async<sizeof(Piece)>(to + 2 * kHeadThreads, next_g + c0[0]);
+          if (on1[0]) copy_async<sizeof(Piece)>(to + 3 * kHeadThreads, next_g + c1[0]);
+          next_g += A.gs[next.kind][2];
+        }
+        if (++next_h == next.h1) {
+          next_it += stride;
+          if (next_it < items) open();
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  int slot = 0;
+  if constexpr (kAsync) {
+    for (int i = 0; i < kSlots * kPieces; ++i) slots[i * kHeadThreads] = Piece{};   // pieces that do not exist stay zero
+    if (next_it < items) open();
+    for (int i = 0; i < kSlots - 1; ++i) fetch(i);
   }
 
+  auto position_of = [&](long long it) {
+    if (!pairs || it >= items) return 0LL;
+    return A.positions[A.items_fit ? (long long)((unsigned)it / (unsigned)per_token) : it / per_token];
+  };
+  long long next_pos = position_of(first);   // (a load ahead, or each item would begin with a wait for it)
   for (long long it = first; it < items; it += stride) {
-    const long long row = it / per_token;
-    int blk = (int)(it - row * per_token);
-    int kind = kind0;
-    if (!GRAD && blk >= A.blocks[0]) {
-      kind = 1;
-      blk -= A.blocks[0];
-    }
-    const long long b = row / A.tokens, t = row - b * A.tokens;
-    const int h0 = blk * A.hb, h1 = min(A.heads[kind], h0 + A.hb);
+    HeadsItem cur;
+    cur.at(A, it, kind0, per_token, GRAD);
+    const int kind = cur.kind;
+    const long long pos = next_pos;
+    next_pos = position_of(it + stride);
 
     float cs[NU][VE], sn[NU][VE];   // of the pairs this lane holds
     if (pairs) {
-      const long long pos = A.positions[row];
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
 #pragma unroll
@@ -150,26 +243,34 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
           cs[n][e] = 1.0f;
           sn[n][e] = 0.0f;
           if (live && on0[n]) {
-            turn_cos_sin(s_turn[p], pos, A.m, cs[n][e], sn[n][e]);
+            turn_cos_sin<sizeof(T) == 2 && !GRAD>(s_turn[p], pos, A.m, cs[n][e], sn[n][e]);
             sn[n][e] *= A.sign;
           }
         }
       }
     }
-    float w[2 * NU * VE];
-    if constexpr (NORM) {
-      const void* wp = A.w[kind];
+    const float* wk = s_w + kind * A.dim;   // (registers are short: the weights stay in shared memory)
+    auto weights = [&](int n, int i, float (&w)[VE]) {
+      const int c = i ? c1[n] : c0[n];
+      const bool on = i ? on1[n] : on0[n];
 #pragma unroll
-      for (int n = 0; n < NU; ++n)
+      for (int e = 0; e < VE; ++e) w[e] = 0.0f;
+      if constexpr (VE >= 4) {
+        if (on) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          w[2 * n * VE + e] = on0[n] ? (A.w_f32 ? ((const float*)wp)[c0[n] + e] : to_f<T>(((const T*)wp)[c0[n] + e])) : 0.0f;
-          w[(2 * n + 1) * VE + e] = on1[n] ? (A.w_f32 ? ((const float*)wp)[c1[n] + e] : to_f<T>(((const T*)wp)[c1[n] + e])) : 0.0f;
+          for (int e = 0; e < VE; e += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(wk + c + e);
+            w[e] = f.x;
+            w[e + 1] = f.y;
+            w[e + 2] = f.z;
+            w[e + 3] = f.w;
+          }
         }
-    }
-    const T* xp = (const T*)A.x[kind] + b * A.xs[kind][0] + t * A.xs[kind][1];
-    const T* gp = GRAD ? (const T*)A.g[kind] + b * A.gs[kind][0] + t * A.gs[kind][1] : nullptr;
-    T* yp = (T*)A.y[kind] + b * A.ys[kind][0] + t * A.ys[kind][1];
+      } else if (on) {
+        w[0] = wk[c];
+      }
+    };
+    T* yp = (T*)A.y[kind] + cur.b * A.ys[kind][0] + cur.t * A.ys[kind][1] + cur.h0 * A.ys[kind][2];
 
     // v (two pieces of each unit) turned by sign * angle
     auto rotate = [&](float (&v)[2 * NU][VE]) {
@@ -177,12 +278,12 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
         if (!A.interleaved || VE == 1) {
+          float p[VE], q[VE];
+          mul_vec<VE>(v[2 * n + 1], sn[n], p);
+          mul_vec<VE>(v[2 * n], sn[n], q);
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            const float a = v[2 * n][e], q = v[2 * n + 1][e];
-            v[2 * n][e] = a * cs[n][e] - q * sn[n][e];
-            v[2 * n + 1][e] = q * cs[n][e] + a * sn[n][e];
-          }
+          for (int e = 0; e < VE; ++e) v[2 * n][e] = fmaf(v[2 * n][e], cs[n][e], -p[e]);
+          fma_vec<VE>(v[2 * n + 1], cs[n], q, v[2 * n + 1]);
         } else {
 #pragma unroll
           for (int e = 0; e < VE / 2; ++e) {
@@ -201,57 +302,84 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
       for (int o = group >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
       return v;
     };
-    auto load = [&](const T* p, float (&v)[2 * NU][VE]) {
+    // vector h of x (which = 0) or of the gradient (1)
+    auto load = [&](int h, int which, float (&v)[2 * NU][VE]) {
+      if constexpr (kAsync) {
 #pragma unroll
-      for (int n = 0; n < NU; ++n) {
+        for (int i = 0; i < 2; ++i) {
+          VecOf<T, VE> u;
+          u.raw = slots[(slot * kPieces + 2 * which + i) * kHeadThreads];
+          u.widen(v[i]);
+        }
+      } else {
+        const long long* st = which ? A.gs[kind] : A.xs[kind];
+        const T* p = (const T*)(which ? A.g[kind] : A.x[kind]) + cur.b * st[0] + cur.t * st[1] + h * st[2];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) v[2 * n][e] = v[2 * n + 1][e] = 0.0f;
-        if (on0[n]) ld_vec<T, VE>(p + c0[n], v[2 * n]);
-        if (on1[n]) ld_vec<T, VE>(p + c1[n], v[2 * n + 1]);
+        for (int n = 0; n < NU; ++n) {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) v[2 * n][e] = v[2 * n + 1][e] = 0.0f;
+          if (on0[n]) ld_vec<T, VE>(p + c0[n], v[2 * n]);
+          if (on1[n]) ld_vec<T, VE>(p + c1[n], v[2 * n + 1]);
+        }
       }
     };
 
-    for (int h = h0; h < h1; ++h) {
+    for (int h = cur.h0; h < cur.h1; ++h) {
+      if constexpr (kAsync) {
+        fetch(slot ? slot - 1 : kSlots - 1);   // the slot read last
+        asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+      }
       float x[2 * NU][VE];
-      load(xp + (long long)h * A.xs[kind][2], x);
+      load(h, 0, x);
       float r = 1.0f;
       if constexpr (NORM) {
-        float ss = 0.0f;
+        unsigned long long s2 = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * NU; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) ss = fmaf(x[i][e], x[i][e], ss);
-        r = rsqrtf(sum_group(ss) / (float)A.dim + A.eps);
+        for (int i = 0; i < 2 * NU; ++i) dot_vec<VE>(x[i], x[i], s2);
+        float s0, s1;
+        unpack2(s2, s0, s1);
+        r = rsqrtf(fmaf(sum_group(s0 + s1), A.inv_dim, A.eps));
       }
       if constexpr (GRAD) {
         float g[2 * NU][VE];
-        load(gp + (long long)h * A.gs[kind][2], g);
+        load(h, 1, g);
         rotate(g);
-        float un = 0.0f;
+        unsigned long long u2 = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * NU; ++i)
+        for (int i = 0; i < 2 * NU; ++i) {
+          scale_vec<VE>(r, x[i]);                       // n
+          fma_vec<VE>(g[i], x[i], dw[i], dw[i]);
+          float w[VE];
+          weights(i >> 1, i & 1, w);
+          mul_vec<VE>(g[i], w, g[i]);                   // u
+          dot_vec<VE>(g[i], x[i], u2);
+        }
+        float u0, u1;
+        unpack2(u2, u0, u1);
+        const float un = -sum_group(u0 + u1) * A.inv_dim;
+        float m[VE];
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            x[i][e] *= r;
-            dw[i * VE + e] = fmaf(g[i][e], x[i][e], dw[i * VE + e]);
-            g[i][e] *= w[i * VE + e];
-            un = fmaf(g[i][e], x[i][e], un);
-          }
-        un = sum_group(un) / (float)A.dim;
+        for (int e = 0; e < VE; ++e) m[e] = un;
 #pragma unroll
-        for (int i = 0; i < 2 * NU; ++i)
-#pragma unroll
-          for (int e = 0; e < VE; ++e) x[i][e] = r * (g[i][e] - x[i][e] * un);
+        for (int i = 0; i < 2 * NU; ++i) {
+          fma_vec<VE>(x[i], m, g[i], x[i]);
+          scale_vec<VE>(r, x[i]);
+        }
       } else {
         if constexpr (NORM) {
 #pragma unroll
-          for (int i = 0; i < 2 * NU; ++i)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[i][e] *= r * w[i * VE + e];
+          for (int i = 0; i < 2 * NU; ++i) {
+            scale_vec<VE>(r, x[i]);
+            float w[VE];
+            weights(i >> 1, i & 1, w);
+            mul_vec<VE>(x[i], w, x[i]);
+          }
         }
         rotate(x);
       }
-      T* o = yp + (long long)h * A.ys[kind][2];
+      T* o = yp;
+      yp += A.ys[kind][2];
+      if constexpr (kAsync) slot = slot + 1 == kSlots ? 0 : slot + 1;
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
         if (on0[n]) st_vec<T, VE>(o + c0[n], x[2 * n]);
@@ -262,12 +390,14 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const __grid_consta
 
   if constexpr (GRAD) {
     // this CTA's sums, in the order of its groups
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < NU; ++n)
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        if (on0[n]) s_dw[sub * A.dim + c0[n] + e] = dw[2 * n * VE + e];
-        if (on1[n]) s_dw[sub * A.dim + c1[n] + e] = dw[(2 * n + 1) * VE + e];
+        if (on0[n]) s_dw[sub * A.dim + c0[n] + e] = dw[2 * n][e];
+        if (on1[n]) s_dw[sub * A.dim + c1[n] + e] = dw[2 * n + 1][e];
       }
     __syncthreads();
     for (int j = threadIdx.x; j < A.dim; j += kHeadThreads) {
@@ -326,6 +456,10 @@ void grad_grid(long long rows, int Hq, int Hk, int* gq, int* gk) {
 
 template <typename T, int VE, int NU, bool NORM, bool GRAD>
 cudaError_t launch_heads(const HeadsArgs& A, int grid, int group, size_t smem, cudaStream_t st) {
+  if (smem > 40 * 1024) {   // (48 KB with what the kernel has of its own)
+    const cudaError_t e = cudaFuncSetAttribute(heads_kernel<T, VE, NU, NORM, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   heads_kernel<T, VE, NU, NORM, GRAD><<<grid, kHeadThreads, smem, st>>>(A, group);
   return cudaGetLastError();
 }
@@ -404,6 +538,8 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
   A.sign = sign;
   A.m = r ? r->factor : 1.0f;
   A.eps = eps;
+  A.inv_dim = 1.0f / (float)dim;
+  A.items_fit = rows * (Hq + Hk) < (1LL << 30);
   A.w_f32 = w_dtype == PN_F32;
   A.positions = positions;
   A.w[0] = wq;
@@ -449,7 +585,7 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
   const int per_cta = kHeadThreads / group;
   const long long vectors = rows * (Hq + Hk);
   int hb = 1;
-  while (hb < 16 && vectors / (2 * hb) >= 148LL * 4 * per_cta) hb <<= 1;
+  while (hb < 8 && vectors / (2 * hb) >= 148LL * 4 * per_cta) hb <<= 1;
   A.hb = hb;
   A.blocks[0] = (Hq + hb - 1) / hb;
   A.blocks[1] = (Hk + hb - 1) / hb;
@@ -460,7 +596,6 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
     int gk_ = 0;
     grad_grid(rows, Hq, Hk, &A.grid_q, &gk_);
     grid = A.grid_q + gk_;
-    smem = (size_t)per_cta * dim * sizeof(float);
     const size_t need = (size_t)grid * dim * sizeof(float);
     if (ws_bytes < need) return seq_fail(PN_ERR_INVALID, "workspace of %zu bytes, %zu needed", ws_bytes, need);
     if (pn_status e = seq_device(ws, "workspace", &dev)) return e;
@@ -470,6 +605,9 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
     const long long items = rows * (A.blocks[0] + A.blocks[1]);
     grid = (int)std::min<long long>((items + per_cta - 1) / per_cta, 148LL * 16);
   }
+  // the slots; the gradient's sums lie in the same memory
+  smem = ve == 1 ? 0 : (size_t)ahead(grad) * (grad ? 4 : 2) * kHeadThreads * ve * es;
+  if (grad) smem = std::max(smem, (size_t)per_cta * dim * sizeof(float));
   cudaError_t e = dtype == PN_F32    ? launch_type<float>(A, ve, norm, grad, grid, group, smem, st)
                   : dtype == PN_BF16 ? launch_type<__nv_bfloat16>(A, ve, norm, grad, grid, group, smem, st)
                                      : launch_type<__half>(A, ve, norm, grad, grid, group, smem, st);

@@ -155,6 +155,12 @@ cudaError_t run_pass(const pn_linattn_s* h, LinPass P, int n_seq, long long max_
   cudaError_t e;
   if (try_tc(h, P, G, max_len, st, &e)) return e;
   P.nseg = fma_parts(h, n_seq, max_len, P.da, P.dc);
+  auto aligned = [](const void* p, long long bs, long long ts, long long hs, size_t es) {
+    return (uintptr_t)p % (4 * es) == 0 && bs % 4 == 0 && ts % 4 == 0 && hs % 4 == 0;
+  };
+  const size_t es = dtype_size(h->dtype);
+  P.vec = aligned(P.out, P.out_bs, P.out_ts, P.out_hs, P.out_f32 ? 4 : es);
+  for (const LinOperand* x : {&P.a, &P.b, &P.c}) P.vec = P.vec && aligned(x->p, x->bs, x->ts, x->hs, es);
   switch (h->dtype) {
     case PN_F32: return launch_pass<float>(P, G, st);
     case PN_BF16: return launch_pass<__nv_bfloat16>(P, G, st);

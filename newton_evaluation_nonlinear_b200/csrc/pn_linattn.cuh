@@ -37,6 +37,7 @@ struct LinPass {
   long long out_bs, out_ts, out_hs;
   int out_f32;             // out is float32 (partial gradients of shared heads)
   int out_map;             // whole chunks of out are stored by TMA
+  int vec;                 // every row of the four arrays is aligned to four elements
   int da, dc;              // widths: a and b, c and out
   int H, n_seq;
   long long T;             // rows of a sequence (no cu), or of the whole buffer
@@ -83,6 +84,24 @@ __device__ __forceinline__ int lin_seg_len(int len, int nseg, int C) {
 // exp2(n * l), n >= 0: one for n = 0 whatever l
 __device__ __forceinline__ float lin_pow(float l, int n) { return n <= 0 ? 1.0f : exp2f(l * (float)n); }
 
+// four neighbours, at once where the arrays allow (vec)
+template <typename T> __device__ __forceinline__ void lin_load4(const T* p, int vec, float (&v)[4]) {
+  if (vec) {
+    ld_vec<T, 4>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_f<T>(p[i]);
+  }
+}
+template <typename T> __device__ __forceinline__ void lin_store4(T* p, int vec, const float (&v)[4]) {
+  if (vec) {
+    st_vec<T, 4>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = from_f<T>(v[i]);
+  }
+}
+
 constexpr int kLinThreads = 256;
 constexpr int kLinDC = 64;     // columns of c one CTA takes
 
@@ -104,9 +123,10 @@ struct LinFmaCfg {
 };
 
 // One CTA: one (sequence, head, part, 64 columns of c), its chunks in turn; the
-// four products of a chunk as 16 x 16 threads with a register tile each, both
-// operands read along their rows.  STATE_ONLY leaves out the outputs: what the
-// part adds to the state, from zero.
+// four products of a chunk by 16 x 16 threads with 4 x 4 values each (2 x 4 where a
+// chunk has 32 rows), both operands read as four neighbours at once.  Bound by the
+// FP32 units and by shared memory, three wavefronts for sixteen FMA.  STATE_ONLY
+// leaves out the outputs: what the part adds to the state, from zero.
 template <typename T, int C, int DA, bool STATE_ONLY>
 __global__ void __launch_bounds__(kLinThreads) lin_fma_kernel(const __grid_constant__ LinPass P,
                                                               const __grid_constant__ LinDecay G) {
@@ -163,116 +183,143 @@ __global__ void __launch_bounds__(kLinThreads) lin_fma_kernel(const __grid_const
   for (int r0 = lo; r0 < hi; r0 += C) {
     const int n = hi - r0 < C ? hi - r0 : C;   // rows of this chunk
     auto row_of = [&](int i) { return start + (P.reverse ? len - 1 - (r0 + i) : r0 + i); };
-    for (int e = tid; e < C * DA; e += kLinThreads) {
-      const int i = e / DA, d = e % DA;
-      float av = 0.0f, bv = 0.0f;
+    // a^T and b^T, b towards the chunk's end, and c: four columns of a row to a thread, eight rows and four such
+    // neighbours to a warp (whole sectors of memory, and no more than two rows of a bank when written transposed)
+    for (int e = tid; e < C * DA / 4; e += kLinThreads) {
+      const int i = (e & 7) + 8 * (e / (2 * DA)), d = 4 * ((e >> 3) % (DA / 4));
+      float av[4] = {}, bv[4] = {};
       if (i < n && d < da) {
         const long long r = row_of(i);
-        if (!STATE_ONLY) av = to_f<T>(ap[r * P.a.ts + d]);
-        bv = to_f<T>(bp[r * P.b.ts + d]);
+        if (!STATE_ONLY) lin_load4<T>(ap + r * P.a.ts + d, P.vec, av);
+        lin_load4<T>(bp + r * P.b.ts + d, P.vec, bv);
       }
-      if (!STATE_ONLY) {
-        sAT[d * K::PC + i] = av;
-        sBT[d * K::PC + i] = bv;
+      const float f = i < n ? P.alpha * sL[n - 1 - i] : 0.0f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (!STATE_ONLY) {
+          sAT[(d + x) * K::PC + i] = av[x];
+          sBT[(d + x) * K::PC + i] = bv[x];
+        }
+        bv[x] *= f;
       }
-      sBW[i * K::PA + d] = i < n ? bv * (P.alpha * sL[n - 1 - i]) : 0.0f;
+      *reinterpret_cast<float4*>(sBW + i * K::PA + d) = make_float4(bv[0], bv[1], bv[2], bv[3]);
     }
-    for (int e = tid; e < C * kLinDC; e += kLinThreads) {
-      const int i = e / kLinDC, j = e % kLinDC;
-      sC[i * K::PV + j] = (i < n && dc0 + j < dc) ? to_f<T>(cp[row_of(i) * P.c.ts + dc0 + j]) : 0.0f;
+    for (int e = tid; e < C * kLinDC / 4; e += kLinThreads) {
+      const int i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
+      float v[4] = {};
+      if (i < n && dc0 + j < dc) lin_load4<T>(cp + row_of(i) * P.c.ts + dc0 + j, P.vec, v);
+      *reinterpret_cast<float4*>(sC + i * K::PV + j) = make_float4(v[0], v[1], v[2], v[3]);
     }
     __syncthreads();
 
-    constexpr int RM = C / 16;   // rows of a register tile (4 or 2)
+    constexpr int RM = C / 16;   // rows of a thread's values (4 or 2)
+    auto rows4 = [](const float* p, float (&x)[RM]) {
+      if constexpr (RM == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        x[0] = f.x;
+        x[1] = f.y;
+        x[2] = f.z;
+        x[3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(p);
+        x[0] = f.x;
+        x[1] = f.y;
+      }
+    };
     if (!STATE_ONLY) {
       // products of rows i = ty RM .. and j = tx RM ..
       float acc[RM][RM] = {};
+#pragma unroll 4
       for (int d = 0; d < da; ++d) {
         float x[RM], y[RM];
-#pragma unroll
-        for (int u = 0; u < RM; ++u) {
-          x[u] = sAT[d * K::PC + ty * RM + u];
-          y[u] = sBT[d * K::PC + tx * RM + u];
-        }
+        rows4(sAT + d * K::PC + ty * RM, x);
+        rows4(sBT + d * K::PC + tx * RM, y);
 #pragma unroll
         for (int u = 0; u < RM; ++u)
 #pragma unroll
           for (int w = 0; w < RM; ++w) acc[u][w] = fmaf(x[u], y[w], acc[u][w]);
       }
 #pragma unroll
-      for (int u = 0; u < RM; ++u)
-#pragma unroll
-        for (int w = 0; w < RM; ++w) {
-          const int i = ty * RM + u, j = tx * RM + w;
-          sPT[j * K::PC + i] = (j <= i && i < n) ? acc[u][w] * (P.alpha * sL[i - j]) : 0.0f;
-        }
-      __syncthreads();
-      float o[RM][4] = {};
-      for (int d = 0; d < da; ++d) {
-        float x[RM];
-#pragma unroll
-        for (int u = 0; u < RM; ++u) x[u] = sAT[d * K::PC + ty * RM + u];
-        const float4 y = *reinterpret_cast<const float4*>(sS + d * K::PV + tx * 4);
+      for (int w = 0; w < RM; ++w) {
+        const int j = tx * RM + w;
+        float p[RM];
 #pragma unroll
         for (int u = 0; u < RM; ++u) {
-          o[u][0] = fmaf(x[u], y.x, o[u][0]);
-          o[u][1] = fmaf(x[u], y.y, o[u][1]);
-          o[u][2] = fmaf(x[u], y.z, o[u][2]);
-          o[u][3] = fmaf(x[u], y.w, o[u][3]);
+          const int i = ty * RM + u;
+          p[u] = (j <= i && i < n) ? acc[u][w] * (P.alpha * sL[i - j]) : 0.0f;
         }
+        if constexpr (RM == 4) *reinterpret_cast<float4*>(sPT + j * K::PC + ty * RM) = make_float4(p[0], p[1], p[2], p[3]);
+        else *reinterpret_cast<float2*>(sPT + j * K::PC + ty * RM) = make_float2(p[0], p[1]);
       }
+      __syncthreads();
+      float o[RM][4] = {};
+      auto product = [&](const float* xs, const float* ys, int k) {   // x [k][rows] times y [k][columns]
+#pragma unroll 4
+        for (int d = 0; d < k; ++d) {
+          float x[RM];
+          rows4(xs + d * K::PC + ty * RM, x);
+          const float4 y = *reinterpret_cast<const float4*>(ys + d * K::PV + tx * 4);
+#pragma unroll
+          for (int u = 0; u < RM; ++u) {
+            o[u][0] = fmaf(x[u], y.x, o[u][0]);
+            o[u][1] = fmaf(x[u], y.y, o[u][1]);
+            o[u][2] = fmaf(x[u], y.z, o[u][2]);
+            o[u][3] = fmaf(x[u], y.w, o[u][3]);
+          }
+        }
+      };
+      product(sAT, sS, da);
 #pragma unroll
       for (int u = 0; u < RM; ++u) {
-        const float f = sL[ty * RM + u + 1 - e0];
+        const float f = sL[max(ty * RM + u + 1 - e0, 0)];
 #pragma unroll
         for (int w = 0; w < 4; ++w) o[u][w] *= f;
       }
-      for (int j = 0; j < n; ++j) {
-        float x[RM];
-#pragma unroll
-        for (int u = 0; u < RM; ++u) x[u] = sPT[j * K::PC + ty * RM + u];
-        const float4 y = *reinterpret_cast<const float4*>(sC + j * K::PV + tx * 4);
-#pragma unroll
-        for (int u = 0; u < RM; ++u) {
-          o[u][0] = fmaf(x[u], y.x, o[u][0]);
-          o[u][1] = fmaf(x[u], y.y, o[u][1]);
-          o[u][2] = fmaf(x[u], y.z, o[u][2]);
-          o[u][3] = fmaf(x[u], y.w, o[u][3]);
-        }
-      }
+      // (a warp's last row is (ty | 1) RM + RM - 1: no row of it takes a later one)
+      product(sPT, sC, min(n, (ty | 1) * RM + RM));
 #pragma unroll
       for (int u = 0; u < RM; ++u) {
         const int i = ty * RM + u;
         if (i < n) {
           const long long at = (P.cu ? 0 : s * P.out_bs) + row_of(i) * P.out_ts + (long long)h * P.out_hs + dc0 + tx * 4;
+          float v[4];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            if (dc0 + tx * 4 + w < dc) {
-              if (P.out_f32) ((float*)P.out)[at + w] = P.beta * o[u][w];
-              else ((T*)P.out)[at + w] = from_f<T>(P.beta * o[u][w]);
-            }
+          for (int w = 0; w < 4; ++w) v[w] = P.beta * o[u][w];
+          if (dc0 + tx * 4 < dc) {
+            if (P.out_f32) lin_store4<float>((float*)P.out + at, P.vec, v);
+            else lin_store4<T>((T*)P.out + at, P.vec, v);
           }
         }
       }
       __syncthreads();   // S is read; it changes below
     }
-    // S: thread (ty, tx) takes rows ty + 16 m and columns tx * 4 ..
+    // S: thread (ty, tx) takes rows 4 ty .. of every 64, and columns tx * 4 ..
     const float f = sL[n - e0];
-    for (int d = ty; d < da; d += 16) {
-      float4 v = *reinterpret_cast<float4*>(sS + d * K::PV + tx * 4);
-      v.x *= f;
-      v.y *= f;
-      v.z *= f;
-      v.w *= f;
-      for (int j = 0; j < n; ++j) {
-        const float x = sBW[j * K::PA + d];
-        const float4 y = *reinterpret_cast<const float4*>(sC + j * K::PV + tx * 4);
-        v.x = fmaf(x, y.x, v.x);
-        v.y = fmaf(x, y.y, v.y);
-        v.z = fmaf(x, y.z, v.z);
-        v.w = fmaf(x, y.w, v.w);
+    for (int d = 4 * ty; d < da; d += 64) {
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] = *reinterpret_cast<const float4*>(sS + (d + u) * K::PV + tx * 4);
+        v[u].x *= f;
+        v[u].y *= f;
+        v[u].z *= f;
+        v[u].w *= f;
       }
-      *reinterpret_cast<float4*>(sS + d * K::PV + tx * 4) = v;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float4 x4 = *reinterpret_cast<const float4*>(sBW + j * K::PA + d);
+        const float4 y = *reinterpret_cast<const float4*>(sC + j * K::PV + tx * 4);
+        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[u].x = fmaf(x[u], y.x, v[u].x);
+          v[u].y = fmaf(x[u], y.y, v[u].y);
+          v[u].z = fmaf(x[u], y.z, v[u].z);
+          v[u].w = fmaf(x[u], y.w, v[u].w);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) *reinterpret_cast<float4*>(sS + (d + u) * K::PV + tx * 4) = v[u];
     }
     __syncthreads();
     e0 = 0;
@@ -433,7 +480,7 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_con
       const long long pos = P.positions[b];
       for (int p = lane; p < P.pairs; p += 32) {
         float c, sn;
-        turn_cos_sin(P.turn[p], pos, P.m, c, sn);
+        turn_cos_sin<false>(P.turn[p], pos, P.m, c, sn);
         const int i0 = P.interleaved ? 2 * p : p, i1 = P.interleaved ? 2 * p + 1 : p + P.pairs;
         const float x0 = dst[i0], x1 = dst[i1];
         dst[i0] = x0 * c - x1 * sn;

@@ -1,9 +1,10 @@
 """Rotary positions, norms of queries and keys, and linear attention on the GPU against plain 64-bit implementations.
 
 Tolerances, from the arithmetic.  u is half a step of the output's type (finfo.eps / 2): one rounding at the end.
-- Rotations and norms: sine and cosine carry at most 2^-22 (the angle's conversion to float, half a step of half a turn,
-  times pi, and sincospif's own error), each output adds about 8 roundings of float32 to the largest value of its
-  vector: 2^-20 of it, plus u of the value.
+- Rotations and norms: for float32 sine and cosine carry at most 2^-22 (the angle's conversion to float, half a step of half
+  a turn, times pi, and sincospif's own error) and each output adds about 8 roundings of float32; for the 16-bit types they
+  carry 2^-21.4 and the angle 2^-22.4, together 2^-20.8, and an output takes two of them, sqrt 2 of its pair's size at most:
+  2^-20.3, with four roundings of float32 below 2^-20.  So 2^-20 of the vector's largest value, plus u of the value.
 - Norm gradients of a weight: sums over n rows of terms of one size, in float32: 2^-24 log2(n) + the terms' own 2^-21
   relative errors, of the sum of the terms' magnitudes: 2^-19 of it.
 - Linear attention: A is the output's formula with every factor replaced by its magnitude.  Products, sums and powers of
