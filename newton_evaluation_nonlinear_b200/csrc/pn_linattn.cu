@@ -31,16 +31,15 @@ LinOperand operand(const pn_heads* x, int per) {
   return LinOperand{x->data, x->batch_stride, x->token_stride, x->head_stride, per};
 }
 
-// Rows of one chunk of the FP32 kernels.
-int fma_chunk(int da) { return da <= 128 ? 64 : 32; }
+// Rows of one chunk of the kernels for any type and width.
+int mma_chunk(int da) { return da <= 128 ? 64 : 32; }
 
-// Parts a sequence is cut into: enough CTAs for the card where sequences and heads are few, at least
-// four chunks each (a part costs a second read of two operands).
-int fma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int dc) {
+// Parts a sequence is cut into there: as many as fit the card beside each other (two CTAs on an SM up to width 64), of four
+// chunks at least (a part costs a second read of two operands and half the work).
+int mma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int dc) {
   const long long ctas = (long long)n_seq * h->H * ((dc + kLinDC - 1) / kLinDC);
-  const long long want = (2 * 148 + ctas - 1) / std::max(1LL, ctas);
-  const long long most = max_len / (4 * fma_chunk(da));
-  return (int)std::max(1LL, std::min(want, most));
+  const long long want = 148 * (da <= 64 ? 2 : 1) / std::max(1LL, ctas);
+  return (int)std::max(1LL, std::min(want, max_len / (4 * mma_chunk(da))));
 }
 
 // Parts for the tensor-core kernel: a CTA fills its SM, so as many as fit the card beside each other.
@@ -57,37 +56,37 @@ size_t seg_bytes(const pn_linattn_s* h, int n_seq, long long max_len) {
   int p = 1;
   for (int t = 0; t < 2; ++t) {
     const int da = t ? h->dv : h->dk, dc = t ? h->dk : h->dv;
-    p = std::max(p, std::max(fma_parts(h, n_seq, max_len, da, dc), tc_parts(h, n_seq, max_len, da, dc)));
+    p = std::max(p, std::max(mma_parts(h, n_seq, max_len, da, dc), tc_parts(h, n_seq, max_len, da, dc)));
   }
   return p > 1 ? align256((size_t)n_seq * h->H * p * h->dk * h->dv * sizeof(float)) : 0;
 }
 
 template <typename T, int C, int DA>
-cudaError_t launch_fma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
-  using K = LinFmaCfg<C, DA>;
+cudaError_t launch_mma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
+  using K = LinMmaCfg<C, DA>;
   const dim3 grid((P.dc + kLinDC - 1) / kLinDC, P.nseg, P.n_seq * P.H);
   cudaError_t e;
   if (P.nseg > 1) {
-    if ((e = cudaFuncSetAttribute(lin_fma_kernel<T, C, DA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if ((e = cudaFuncSetAttribute(lin_mma_kernel<T, C, DA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   K::SMEM_BYTES)) != cudaSuccess)
       return e;
-    lin_fma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), kLinThreads, K::SMEM_BYTES, st>>>(P, G);
+    lin_mma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), kLinThreads, K::SMEM_BYTES, st>>>(P, G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, C, 0);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if ((e = cudaFuncSetAttribute(lin_fma_kernel<T, C, DA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if ((e = cudaFuncSetAttribute(lin_mma_kernel<T, C, DA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 K::SMEM_BYTES)) != cudaSuccess)
     return e;
-  lin_fma_kernel<T, C, DA, false><<<grid, kLinThreads, K::SMEM_BYTES, st>>>(P, G);
+  lin_mma_kernel<T, C, DA, false><<<grid, kLinThreads, K::SMEM_BYTES, st>>>(P, G);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_pass(const LinPass& P, const LinDecay& G, cudaStream_t st) {
-  if (P.da <= 64) return launch_fma<T, 64, 64>(P, G, st);
-  if (P.da <= 128) return launch_fma<T, 64, 128>(P, G, st);
-  return launch_fma<T, 32, 256>(P, G, st);
+  if (P.da <= 64) return launch_mma<T, 64, 64>(P, G, st);
+  if (P.da <= 128) return launch_mma<T, 64, 128>(P, G, st);
+  return launch_mma<T, 32, 256>(P, G, st);
 }
 
 // The tensor map of one operand: boxes of 64 rows x 64 columns of one head, 128-byte swizzled.
@@ -128,7 +127,7 @@ cudaError_t launch_tc(const LinMaps& maps, const LinPass& P, const LinDecay& G, 
                    : launch_tc_kernel<T, DA, DC, kLinOut>(maps, P, G, P.nseg, st);
 }
 
-// The tensor-core kernel, where it can take the pass; false where the FP32 kernel has to.
+// The tensor-core kernel, where it can take the pass; false where the other one has to.
 bool try_tc(const pn_linattn_s* h, LinPass& P, const LinDecay& G, long long max_len, cudaStream_t st, cudaError_t* e) {
   if (h->dtype != PN_BF16 || P.da > 128 || P.T < 1) return false;
   LinMaps maps;
@@ -154,7 +153,7 @@ cudaError_t run_pass(const pn_linattn_s* h, LinPass P, int n_seq, long long max_
   P.seg_state = (float*)seg;
   cudaError_t e;
   if (try_tc(h, P, G, max_len, st, &e)) return e;
-  P.nseg = fma_parts(h, n_seq, max_len, P.da, P.dc);
+  P.nseg = mma_parts(h, n_seq, max_len, P.da, P.dc);
   auto aligned = [](const void* p, long long bs, long long ts, long long hs, size_t es) {
     return (uintptr_t)p % (4 * es) == 0 && bs % 4 == 0 && ts % 4 == 0 && hs % 4 == 0;
   };

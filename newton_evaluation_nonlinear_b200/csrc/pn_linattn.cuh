@@ -1,5 +1,5 @@
 // pn_linattn.cuh -- linear attention with a decay for each head: the parameter
-// block of one pass over the rows, and the FP32 kernels.
+// block of one pass over the rows, and the kernels for any type and width.
 //
 //   S_t = e^{g_h} S_{t-1} + alpha b_t c_t^T,   out_t = beta a_t S_t
 //
@@ -106,42 +106,84 @@ constexpr int kLinThreads = 256;
 constexpr int kLinDC = 64;     // columns of c one CTA takes
 
 template <int C, int DA>
-struct LinFmaCfg {
-  static constexpr int PA = DA + 4;        // row strides, a multiple of 4 floats
-  static constexpr int PC = C + 4;
-  static constexpr int PV = kLinDC + 4;
-  static constexpr int OFF_AT = 0;                     // a^T [DA][PC]
-  static constexpr int OFF_BT = OFF_AT + DA * PC;      // b^T [DA][PC]
-  static constexpr int OFF_BW = OFF_BT + DA * PC;      // b, decayed to the chunk's end [C][PA]
-  static constexpr int OFF_C = OFF_BW + C * PA;        // c [C][PV]
-  static constexpr int OFF_PT = OFF_C + C * PV;        // masked, decayed products, transposed [C][PC]
-  static constexpr int OFF_S = OFF_PT + C * PC;        // S [DA][PV]
+struct LinMmaCfg {
+  // Row strides in floats.  Fragments read rows (lane >> 2) and columns (lane & 3) of an A operand, and the other way round
+  // of a B operand: strides of 12 and 8 banks keep both free of conflicts.
+  static constexpr int PA = DA + 12;
+  static constexpr int PV = kLinDC + 8;
+  static constexpr int PP = C + 4;
+  static constexpr int OFF_A = 0;                      // a [C][PA]
+  static constexpr int OFF_B = OFF_A + C * PA;         // b [C][PA]
+  static constexpr int OFF_C = OFF_B + C * PA;         // c [C][PV]
+  static constexpr int OFF_W = OFF_C + C * PV;         // c, decayed to the chunk's end [C][PV]
+  static constexpr int OFF_P = OFF_W + C * PV;         // masked, decayed products [C][PP]
+  static constexpr int OFF_S = OFF_P + C * PP;         // S [DA][PV]
   static constexpr int OFF_L = OFF_S + DA * PV;        // powers [C + 1]
-  static constexpr int FLOATS = OFF_L + C + 4;
-  static constexpr int SMEM_BYTES = FLOATS * 4;
+  static constexpr int SMEM_BYTES = (OFF_L + C + 4) * 4;
+  static constexpr int CTAS = SMEM_BYTES <= 112 * 1024 ? 2 : 1;   // on an SM
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  // warps: RT x CG over P's and the outputs' rows (16 each) and columns; MW x SG over S's
+  static constexpr int RT = C / 16, CG = 8 / RT;
+  static constexpr int NP = C / 8 / CG, NO = kLinDC / 8 / CG;
+  static constexpr int MT = DA / 16, MW = MT < 8 ? MT : 8, SG = 8 / MW, MS = MT / MW, NS = kLinDC / 8 / SG;
 };
 
+// D += A B, 16 x 8 x 8 in TF32.  Lane (g, t) = (lane >> 2, lane & 3) holds rows g, g + 8 and columns t, t + 4 of A, rows
+// t, t + 4 and column g of B, rows g, g + 8 and columns 2t, 2t + 1 of D.
+__device__ __forceinline__ void lin_mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+// An operand's fragment as the TF32 value nearest to it and, where TF32 does not hold it (SPLIT), what is left.
+template <int N, bool SPLIT>
+struct LinFrag {
+  uint32_t hi[N], lo[SPLIT ? N : 1];
+  __device__ __forceinline__ void set(int i, float x) {
+    if constexpr (SPLIT) {
+      uint32_t r;
+      asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+      hi[i] = r;
+      lo[i] = __float_as_uint(x - __uint_as_float(r));
+    } else {
+      hi[i] = __float_as_uint(x);
+    }
+  }
+};
+// Their product: hi hi + hi lo + lo hi (22 bits of each factor).
+template <bool SA, bool SB>
+__device__ __forceinline__ void lin_mma_split(float (&d)[4], const LinFrag<4, SA>& a, const LinFrag<2, SB>& b) {
+  if constexpr (SA) lin_mma(d, a.lo, b.hi);
+  if constexpr (SB) lin_mma(d, a.hi, b.lo);
+  lin_mma(d, a.hi, b.hi);
+}
+
 // One CTA: one (sequence, head, part, 64 columns of c), its chunks in turn; the
-// four products of a chunk by 16 x 16 threads with 4 x 4 values each (2 x 4 where a
-// chunk has 32 rows), both operands read as four neighbours at once.  Bound by the
-// FP32 units and by shared memory, three wavefronts for sixteen FMA.  STATE_ONLY
-// leaves out the outputs: what the part adds to the state, from zero.
+// four products of a chunk by eight warps on the TF32 tensor cores (mma.sync), in
+// split form: 16-bit operands are TF32 values as they are, everything else takes two.
+// S is summed in float32 registers (the tensor cores truncate) and copied to
+// shared memory for the outputs.  What it is for is float32, which the tcgen05 kernel
+// does not take: 4 x 16 heads x 4096 rows of width 64 took 616 us by FP32 FMA with
+// 4 x 4 values a thread, which shared memory bounds, and take MEASURE us so.
+// STATE_ONLY leaves out the outputs: what the part adds to the state, from zero.
 template <typename T, int C, int DA, bool STATE_ONLY>
-__global__ void __launch_bounds__(kLinThreads) lin_fma_kernel(const __grid_constant__ LinPass P,
-                                                              const __grid_constant__ LinDecay G) {
-  using K = LinFmaCfg<C, DA>;
+__global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_kernel(const __grid_constant__ LinPass P,
+                                                                                     const __grid_constant__ LinDecay G) {
+  using K = LinMmaCfg<C, DA>;
+  constexpr bool X = sizeof(T) == 4;   // inputs are split
   extern __shared__ __align__(16) float smem_lin[];
-  float* sAT = smem_lin + K::OFF_AT;
-  float* sBT = smem_lin + K::OFF_BT;
-  float* sBW = smem_lin + K::OFF_BW;
+  float* sA = smem_lin + K::OFF_A;
+  float* sB = smem_lin + K::OFF_B;
   float* sC = smem_lin + K::OFF_C;
-  float* sPT = smem_lin + K::OFF_PT;
+  float* sW = smem_lin + K::OFF_W;
+  float* sP = smem_lin + K::OFF_P;
   float* sS = smem_lin + K::OFF_S;
   float* sL = smem_lin + K::OFF_L;
 
-  const int tid = threadIdx.x;
-  const int tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
   const int dc0 = blockIdx.x * kLinDC;
   const int seg = blockIdx.y;
   const int sh = blockIdx.z;
@@ -164,180 +206,214 @@ __global__ void __launch_bounds__(kLinThreads) lin_fma_kernel(const __grid_const
   const T* bp = (const T*)P.b.p + (P.cu ? 0 : s * P.b.bs) + (long long)(h / P.b.per) * P.b.hs;
   const T* cp = (const T*)P.c.p + (P.cu ? 0 : s * P.c.bs) + (long long)(h / P.c.per) * P.c.hs;
 
+  // this warp's part of S: rows 16 (sm + 8 x) + g (+ 8), columns 8 (sn0 + y) + 2 t (+ 1)
+  const int sm = warp % K::MW, sn0 = warp / K::MW * K::NS;
+  auto s_row = [&](int x, int e) { return 16 * (sm + 8 * x) + g + (e & 2) * 4; };
+  auto s_col = [&](int y, int e) { return 8 * (sn0 + y) + 2 * t + (e & 1); };
+  float S[K::MS][K::NS][4];
   // what enters: the caller's state, or what the parts before left (STATE_ONLY: nothing)
   const long long mat = (long long)sh * da * dc;
   const bool from_user = !STATE_ONLY && seg == 0;
-  for (int e = tid; e < DA * kLinDC; e += kLinThreads) {
-    const int i = e / kLinDC, j = e % kLinDC;
-    float v = 0.0f;
-    if (!STATE_ONLY && i < da && dc0 + j < dc) {
-      if (P.nseg > 1) v = P.seg_state[((long long)sh * P.nseg + seg) * da * dc + (long long)i * dc + dc0 + j];
-      else if (P.s_in) v = P.s_in[mat + (long long)i * P.s_row + (long long)(dc0 + j) * P.s_col];
-    }
-    sS[i * K::PV + j] = v;
-  }
+#pragma unroll
+  for (int x = 0; x < K::MS; ++x)
+#pragma unroll
+    for (int y = 0; y < K::NS; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = s_row(x, e), j = dc0 + s_col(y, e);
+        float v = 0.0f;
+        if (!STATE_ONLY && i < da && j < dc) {
+          if (P.nseg > 1) v = P.seg_state[((long long)sh * P.nseg + seg) * da * dc + (long long)i * dc + j];
+          else if (P.s_in) v = P.s_in[mat + (long long)i * P.s_row + (long long)j * P.s_col];
+        }
+        S[x][y][e] = v;
+      }
+  auto publish = [&]() {   // S to shared memory
+#pragma unroll
+    for (int x = 0; x < K::MS; ++x)
+#pragma unroll
+      for (int y = 0; y < K::NS; ++y) {
+        *reinterpret_cast<float2*>(sS + s_row(x, 0) * K::PV + s_col(y, 0)) = make_float2(S[x][y][0], S[x][y][1]);
+        *reinterpret_cast<float2*>(sS + s_row(x, 2) * K::PV + s_col(y, 0)) = make_float2(S[x][y][2], S[x][y][3]);
+      }
+  };
+  if (!STATE_ONLY) publish();
   for (int n = tid; n <= C; n += kLinThreads) sL[n] = lin_pow(l2, n);
   __syncthreads();
 
+  const int wr = warp % K::RT, wc = warp / K::RT;
   int e0 = (from_user && P.reverse) ? 1 : 0;   // the state that enters against time is not decayed by its first row
   for (int r0 = lo; r0 < hi; r0 += C) {
     const int n = hi - r0 < C ? hi - r0 : C;   // rows of this chunk
     auto row_of = [&](int i) { return start + (P.reverse ? len - 1 - (r0 + i) : r0 + i); };
-    // a^T and b^T, b towards the chunk's end, and c: four columns of a row to a thread, eight rows and four such
-    // neighbours to a warp (whole sectors of memory, and no more than two rows of a bank when written transposed)
     for (int e = tid; e < C * DA / 4; e += kLinThreads) {
-      const int i = (e & 7) + 8 * (e / (2 * DA)), d = 4 * ((e >> 3) % (DA / 4));
+      const int i = e / (DA / 4), d = 4 * (e % (DA / 4));
       float av[4] = {}, bv[4] = {};
       if (i < n && d < da) {
         const long long r = row_of(i);
         if (!STATE_ONLY) lin_load4<T>(ap + r * P.a.ts + d, P.vec, av);
         lin_load4<T>(bp + r * P.b.ts + d, P.vec, bv);
       }
-      const float f = i < n ? P.alpha * sL[n - 1 - i] : 0.0f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (!STATE_ONLY) {
-          sAT[(d + x) * K::PC + i] = av[x];
-          sBT[(d + x) * K::PC + i] = bv[x];
-        }
-        bv[x] *= f;
-      }
-      *reinterpret_cast<float4*>(sBW + i * K::PA + d) = make_float4(bv[0], bv[1], bv[2], bv[3]);
+      if (!STATE_ONLY) *reinterpret_cast<float4*>(sA + i * K::PA + d) = make_float4(av[0], av[1], av[2], av[3]);
+      *reinterpret_cast<float4*>(sB + i * K::PA + d) = make_float4(bv[0], bv[1], bv[2], bv[3]);
     }
     for (int e = tid; e < C * kLinDC / 4; e += kLinThreads) {
       const int i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
       float v[4] = {};
       if (i < n && dc0 + j < dc) lin_load4<T>(cp + row_of(i) * P.c.ts + dc0 + j, P.vec, v);
-      *reinterpret_cast<float4*>(sC + i * K::PV + j) = make_float4(v[0], v[1], v[2], v[3]);
+      if (!STATE_ONLY) *reinterpret_cast<float4*>(sC + i * K::PV + j) = make_float4(v[0], v[1], v[2], v[3]);
+      const float f = i < n ? P.alpha * sL[n - 1 - i] : 0.0f;
+      *reinterpret_cast<float4*>(sW + i * K::PV + j) = make_float4(f * v[0], f * v[1], f * v[2], f * v[3]);
     }
     __syncthreads();
 
-    constexpr int RM = C / 16;   // rows of a thread's values (4 or 2)
-    auto rows4 = [](const float* p, float (&x)[RM]) {
-      if constexpr (RM == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(p);
-        x[0] = f.x;
-        x[1] = f.y;
-        x[2] = f.z;
-        x[3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(p);
-        x[0] = f.x;
-        x[1] = f.y;
-      }
-    };
     if (!STATE_ONLY) {
-      // products of rows i = ty RM .. and j = tx RM ..
-      float acc[RM][RM] = {};
-#pragma unroll 4
-      for (int d = 0; d < da; ++d) {
-        float x[RM], y[RM];
-        rows4(sAT + d * K::PC + ty * RM, x);
-        rows4(sBT + d * K::PC + tx * RM, y);
+      // products of rows 16 wr .. with rows 8 (wc NP + y) .., up to the diagonal
+      float acc[K::NP][4] = {};
+      const int last = 2 * wr + 1;   // the last column tile that this row tile takes
+#pragma unroll 2
+      for (int k = 0; k < da; k += 8) {
+        LinFrag<4, X> a;
+        const float* pa = sA + (16 * wr + g) * K::PA + k + t;
+        a.set(0, pa[0]);
+        a.set(1, pa[8 * K::PA]);
+        a.set(2, pa[4]);
+        a.set(3, pa[8 * K::PA + 4]);
 #pragma unroll
-        for (int u = 0; u < RM; ++u)
-#pragma unroll
-          for (int w = 0; w < RM; ++w) acc[u][w] = fmaf(x[u], y[w], acc[u][w]);
+        for (int y = 0; y < K::NP; ++y) {
+          if (wc * K::NP + y > last) break;
+          LinFrag<2, X> b;
+          const float* pb = sB + (8 * (wc * K::NP + y) + g) * K::PA + k + t;
+          b.set(0, pb[0]);
+          b.set(1, pb[4]);
+          lin_mma_split<X, X>(acc[y], a, b);
+        }
       }
 #pragma unroll
-      for (int w = 0; w < RM; ++w) {
-        const int j = tx * RM + w;
-        float p[RM];
+      for (int y = 0; y < K::NP; ++y) {
+        if (wc * K::NP + y > last) break;
 #pragma unroll
-        for (int u = 0; u < RM; ++u) {
-          const int i = ty * RM + u;
-          p[u] = (j <= i && i < n) ? acc[u][w] * (P.alpha * sL[i - j]) : 0.0f;
+        for (int e = 0; e < 4; e += 2) {
+          const int i = 16 * wr + g + e * 4, j = 8 * (wc * K::NP + y) + 2 * t;
+          float p[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            p[u] = (j + u <= i && i < n) ? acc[y][e + u] * (P.alpha * sL[i - j - u]) : 0.0f;
+          *reinterpret_cast<float2*>(sP + i * K::PP + j) = make_float2(p[0], p[1]);
         }
-        if constexpr (RM == 4) *reinterpret_cast<float4*>(sPT + j * K::PC + ty * RM) = make_float4(p[0], p[1], p[2], p[3]);
-        else *reinterpret_cast<float2*>(sPT + j * K::PC + ty * RM) = make_float2(p[0], p[1]);
       }
       __syncthreads();
-      float o[RM][4] = {};
-      auto product = [&](const float* xs, const float* ys, int k) {   // x [k][rows] times y [k][columns]
-#pragma unroll 4
-        for (int d = 0; d < k; ++d) {
-          float x[RM];
-          rows4(xs + d * K::PC + ty * RM, x);
-          const float4 y = *reinterpret_cast<const float4*>(ys + d * K::PV + tx * 4);
+      // outputs of rows 16 wr .., columns 8 (wc NO + y) ..: the state's share, then the chunk's
+      float o[K::NO][4] = {};
+      auto product = [&](const float* x, int px, const float* z, int k1, auto split_x, auto split_z) {
+        constexpr bool SX = decltype(split_x)::value, SZ = decltype(split_z)::value;
+#pragma unroll 2
+        for (int k = 0; k < k1; k += 8) {
+          LinFrag<4, SX> a;
+          const float* pa = x + (16 * wr + g) * px + k + t;
+          a.set(0, pa[0]);
+          a.set(1, pa[8 * px]);
+          a.set(2, pa[4]);
+          a.set(3, pa[8 * px + 4]);
 #pragma unroll
-          for (int u = 0; u < RM; ++u) {
-            o[u][0] = fmaf(x[u], y.x, o[u][0]);
-            o[u][1] = fmaf(x[u], y.y, o[u][1]);
-            o[u][2] = fmaf(x[u], y.z, o[u][2]);
-            o[u][3] = fmaf(x[u], y.w, o[u][3]);
+          for (int y = 0; y < K::NO; ++y) {
+            LinFrag<2, SZ> b;
+            const float* pb = z + (k + t) * K::PV + 8 * (wc * K::NO + y) + g;
+            b.set(0, pb[0]);
+            b.set(1, pb[4 * K::PV]);
+            lin_mma_split<SX, SZ>(o[y], a, b);
           }
         }
       };
-      product(sAT, sS, da);
+      using Yes = std::integral_constant<bool, true>;
+      using In = std::integral_constant<bool, X>;
+      product(sA, K::PA, sS, da, In{}, Yes{});
+      const float f0 = sL[max(16 * wr + g + 1 - e0, 0)], f1 = sL[max(16 * wr + g + 9 - e0, 0)];
 #pragma unroll
-      for (int u = 0; u < RM; ++u) {
-        const float f = sL[max(ty * RM + u + 1 - e0, 0)];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) o[u][w] *= f;
+      for (int y = 0; y < K::NO; ++y) {
+        o[y][0] *= f0;
+        o[y][1] *= f0;
+        o[y][2] *= f1;
+        o[y][3] *= f1;
       }
-      // (a warp's last row is (ty | 1) RM + RM - 1: no row of it takes a later one)
-      product(sPT, sC, min(n, (ty | 1) * RM + RM));
+      product(sP, K::PP, sC, min(n, 16 * wr + 16), Yes{}, In{});
 #pragma unroll
-      for (int u = 0; u < RM; ++u) {
-        const int i = ty * RM + u;
-        if (i < n) {
-          const long long at = (P.cu ? 0 : s * P.out_bs) + row_of(i) * P.out_ts + (long long)h * P.out_hs + dc0 + tx * 4;
-          float v[4];
+      for (int e = 0; e < 4; e += 2) {
+        const int i = 16 * wr + g + e * 4;
+        if (i >= n) continue;
+        const long long at = (P.cu ? 0 : s * P.out_bs) + row_of(i) * P.out_ts + (long long)h * P.out_hs + dc0;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) v[w] = P.beta * o[u][w];
-          if (dc0 + tx * 4 < dc) {
-            if (P.out_f32) lin_store4<float>((float*)P.out + at, P.vec, v);
-            else lin_store4<T>((T*)P.out + at, P.vec, v);
+        for (int y = 0; y < K::NO; ++y) {
+          const int j = 8 * (wc * K::NO + y) + 2 * t;
+          if (dc0 + j >= dc) continue;
+          const float v[2] = {P.beta * o[y][e], P.beta * o[y][e + 1]};
+          if (P.out_f32) {
+            float* p = (float*)P.out + at + j;
+            if (P.vec) st_vec<float, 2>(p, v);
+            else p[0] = v[0], p[1] = v[1];
+          } else {
+            T* p = (T*)P.out + at + j;
+            if (P.vec) st_vec<T, 2>(p, v);
+            else p[0] = from_f<T>(v[0]), p[1] = from_f<T>(v[1]);
           }
         }
       }
-      __syncthreads();   // S is read; it changes below
     }
-    // S: thread (ty, tx) takes rows 4 ty .. of every 64, and columns tx * 4 ..
+    // S = e^{g n} S + b^T c'
     const float f = sL[n - e0];
-    for (int d = 4 * ty; d < da; d += 64) {
-      float4 v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        v[u] = *reinterpret_cast<const float4*>(sS + (d + u) * K::PV + tx * 4);
-        v[u].x *= f;
-        v[u].y *= f;
-        v[u].z *= f;
-        v[u].w *= f;
-      }
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const float4 x4 = *reinterpret_cast<const float4*>(sBW + j * K::PA + d);
-        const float4 y = *reinterpret_cast<const float4*>(sC + j * K::PV + tx * 4);
-        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+    for (int x = 0; x < K::MS; ++x) {
+      float u[K::NS][4] = {};
+#pragma unroll 2
+      for (int k = 0; k < n; k += 8) {
+        LinFrag<4, X> a;
+        const float* pa = sB + (k + t) * K::PA + 16 * (sm + 8 * x) + g;
+        a.set(0, pa[0]);
+        a.set(1, pa[8]);
+        a.set(2, pa[4 * K::PA]);
+        a.set(3, pa[4 * K::PA + 8]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          v[u].x = fmaf(x[u], y.x, v[u].x);
-          v[u].y = fmaf(x[u], y.y, v[u].y);
-          v[u].z = fmaf(x[u], y.z, v[u].z);
-          v[u].w = fmaf(x[u], y.w, v[u].w);
+        for (int y = 0; y < K::NS; ++y) {
+          LinFrag<2, true> b;
+          const float* pb = sW + (k + t) * K::PV + 8 * (sn0 + y) + g;
+          b.set(0, pb[0]);
+          b.set(1, pb[4 * K::PV]);
+          lin_mma_split<X, true>(u[y], a, b);
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) *reinterpret_cast<float4*>(sS + (d + u) * K::PV + tx * 4) = v[u];
+      for (int y = 0; y < K::NS; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[x][y][e] = fmaf(f, S[x][y][e], u[y][e]);
     }
-    __syncthreads();
+    __syncthreads();   // everything of this chunk is read
+    if (!STATE_ONLY) publish();
     e0 = 0;
   }
 
+  float* dst = nullptr;
+  long long di = 0, dj = 0;
+  float f = 1.0f;
   if (STATE_ONLY) {
-    float* dst = P.seg_state + ((long long)sh * P.nseg + seg + 1) * da * dc;
-    for (int e = tid; e < da * kLinDC; e += kLinThreads) {
-      const int i = e / kLinDC, j = e % kLinDC;
-      if (dc0 + j < dc) dst[(long long)i * dc + dc0 + j] = sS[i * K::PV + j];
-    }
+    dst = P.seg_state + ((long long)sh * P.nseg + seg + 1) * da * dc;
+    di = dc;
+    dj = 1;
   } else if (P.s_out && owns_end) {
-    // against time the first state's gradient still decays by the first row
-    const float f = (P.reverse && len > 0) ? sL[1] : 1.0f;
-    for (int e = tid; e < da * kLinDC; e += kLinThreads) {
-      const int i = e / kLinDC, j = e % kLinDC;
-      if (dc0 + j < dc) P.s_out[mat + (long long)i * P.s_row + (long long)(dc0 + j) * P.s_col] = f * sS[i * K::PV + j];
-    }
+    dst = P.s_out + mat;
+    di = P.s_row;
+    dj = P.s_col;
+    if (P.reverse && len > 0) f = sL[1];   // against time the first state's gradient still decays by the first row
+  }
+  if (dst) {
+#pragma unroll
+    for (int x = 0; x < K::MS; ++x)
+#pragma unroll
+      for (int y = 0; y < K::NS; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = s_row(x, e), j = dc0 + s_col(y, e);
+          if (i < da && j < dc) dst[(long long)i * di + (long long)j * dj] = f * S[x][y][e];
+        }
   }
 }
 
