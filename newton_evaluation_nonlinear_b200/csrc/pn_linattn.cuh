@@ -125,6 +125,7 @@ struct LinMmaCfg {
   // warps: RT x CG over P's and the outputs' rows (16 each) and columns; MW x SG over S's
   static constexpr int RT = C / 16, CG = 8 / RT;
   static constexpr int NP = C / 8 / CG, NO = kLinDC / 8 / CG;
+  static_assert(C * DA / 4 % (4 * 256) == 0, "whole groups of loads");
   static constexpr int MT = DA / 16, MW = MT < 8 ? MT : 8, SG = 8 / MW, MS = MT / MW, NS = kLinDC / 8 / SG;
 };
 
@@ -152,12 +153,23 @@ struct LinFrag {
     }
   }
 };
-// Their product: hi hi + hi lo + lo hi (22 bits of each factor).
-template <bool SA, bool SB>
-__device__ __forceinline__ void lin_mma_split(float (&d)[4], const LinFrag<4, SA>& a, const LinFrag<2, SB>& b) {
-  if constexpr (SA) lin_mma(d, a.lo, b.hi);
-  if constexpr (SB) lin_mma(d, a.hi, b.lo);
-  lin_mma(d, a.hi, b.hi);
+// Their products: hi hi + hi lo + lo hi (22 bits of each factor), a pass over all N tiles at a time, so that a tile's sum is
+// not waited for by its next term.
+template <int N, bool SA, bool SB>
+__device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4, SA>& a, const LinFrag<2, SB> (&b)[N], int n) {
+  if constexpr (SA) {
+#pragma unroll
+    for (int y = 0; y < N; ++y)
+      if (y < n) lin_mma(d[y], a.lo, b[y].hi);
+  }
+  if constexpr (SB) {
+#pragma unroll
+    for (int y = 0; y < N; ++y)
+      if (y < n) lin_mma(d[y], a.hi, b[y].lo);
+  }
+#pragma unroll
+  for (int y = 0; y < N; ++y)
+    if (y < n) lin_mma(d[y], a.hi, b[y].hi);
 }
 
 // One CTA: one (sequence, head, part, 64 columns of c), its chunks in turn; the
@@ -246,21 +258,41 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
   for (int r0 = lo; r0 < hi; r0 += C) {
     const int n = hi - r0 < C ? hi - r0 : C;   // rows of this chunk
     auto row_of = [&](int i) { return start + (P.reverse ? len - 1 - (r0 + i) : r0 + i); };
-    for (int e = tid; e < C * DA / 4; e += kLinThreads) {
-      const int i = e / (DA / 4), d = 4 * (e % (DA / 4));
-      float av[4] = {}, bv[4] = {};
-      if (i < n && d < da) {
-        const long long r = row_of(i);
-        if (!STATE_ONLY) lin_load4<T>(ap + r * P.a.ts + d, P.vec, av);
-        lin_load4<T>(bp + r * P.b.ts + d, P.vec, bv);
-      }
-      if (!STATE_ONLY) *reinterpret_cast<float4*>(sA + i * K::PA + d) = make_float4(av[0], av[1], av[2], av[3]);
-      *reinterpret_cast<float4*>(sB + i * K::PA + d) = make_float4(bv[0], bv[1], bv[2], bv[3]);
+    // several loads in flight before their values are needed: a thread's 4 x 4 values of a and b at a time, then c's
+    constexpr int kC = C * kLinDC / 4 / kLinThreads;
+    float cv[kC][4];
+#pragma unroll
+    for (int x = 0; x < kC; ++x) {
+      const int e = tid + x * kLinThreads, i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
+#pragma unroll
+      for (int y = 0; y < 4; ++y) cv[x][y] = 0.0f;
+      if (i < n && dc0 + j < dc) lin_load4<T>(cp + row_of(i) * P.c.ts + dc0 + j, P.vec, cv[x]);
     }
-    for (int e = tid; e < C * kLinDC / 4; e += kLinThreads) {
-      const int i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
-      float v[4] = {};
-      if (i < n && dc0 + j < dc) lin_load4<T>(cp + row_of(i) * P.c.ts + dc0 + j, P.vec, v);
+#pragma unroll 1
+    for (int first = tid; first < C * DA / 4; first += 4 * kLinThreads) {
+      float av[4][4], bv[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = first + x * kLinThreads, i = e / (DA / 4), d = 4 * (e % (DA / 4));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) av[x][y] = bv[x][y] = 0.0f;
+        if (i < n && d < da) {
+          const long long r = row_of(i);
+          if (!STATE_ONLY) lin_load4<T>(ap + r * P.a.ts + d, P.vec, av[x]);
+          lin_load4<T>(bp + r * P.b.ts + d, P.vec, bv[x]);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int e = first + x * kLinThreads, i = e / (DA / 4), d = 4 * (e % (DA / 4));
+        if (!STATE_ONLY) *reinterpret_cast<float4*>(sA + i * K::PA + d) = make_float4(av[x][0], av[x][1], av[x][2], av[x][3]);
+        *reinterpret_cast<float4*>(sB + i * K::PA + d) = make_float4(bv[x][0], bv[x][1], bv[x][2], bv[x][3]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < kC; ++x) {
+      const int e = tid + x * kLinThreads, i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
+      const float (&v)[4] = cv[x];
       if (!STATE_ONLY) *reinterpret_cast<float4*>(sC + i * K::PV + j) = make_float4(v[0], v[1], v[2], v[3]);
       const float f = i < n ? P.alpha * sL[n - 1 - i] : 0.0f;
       *reinterpret_cast<float4*>(sW + i * K::PV + j) = make_float4(f * v[0], f * v[1], f * v[2], f * v[3]);
@@ -270,28 +302,27 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
     if (!STATE_ONLY) {
       // products of rows 16 wr .. with rows 8 (wc NP + y) .., up to the diagonal
       float acc[K::NP][4] = {};
-      const int last = 2 * wr + 1;   // the last column tile that this row tile takes
+      const int tiles = min(K::NP, 2 * wr + 2 - wc * K::NP);   // column tiles that this row tile takes
 #pragma unroll 2
-      for (int k = 0; k < da; k += 8) {
+      for (int k = 0; k < (tiles > 0 ? da : 0); k += 8) {
         LinFrag<4, X> a;
         const float* pa = sA + (16 * wr + g) * K::PA + k + t;
         a.set(0, pa[0]);
         a.set(1, pa[8 * K::PA]);
         a.set(2, pa[4]);
         a.set(3, pa[8 * K::PA + 4]);
+        LinFrag<2, X> b[K::NP];
 #pragma unroll
         for (int y = 0; y < K::NP; ++y) {
-          if (wc * K::NP + y > last) break;
-          LinFrag<2, X> b;
           const float* pb = sB + (8 * (wc * K::NP + y) + g) * K::PA + k + t;
-          b.set(0, pb[0]);
-          b.set(1, pb[4]);
-          lin_mma_split<X, X>(acc[y], a, b);
+          b[y].set(0, pb[0]);
+          b[y].set(1, pb[4]);
         }
+        lin_mma_split<K::NP, X, X>(acc, a, b, tiles);
       }
 #pragma unroll
       for (int y = 0; y < K::NP; ++y) {
-        if (wc * K::NP + y > last) break;
+        if (y >= tiles) break;
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const int i = 16 * wr + g + e * 4, j = 8 * (wc * K::NP + y) + 2 * t;
@@ -315,14 +346,14 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
           a.set(1, pa[8 * px]);
           a.set(2, pa[4]);
           a.set(3, pa[8 * px + 4]);
+          LinFrag<2, SZ> b[K::NO];
 #pragma unroll
           for (int y = 0; y < K::NO; ++y) {
-            LinFrag<2, SZ> b;
             const float* pb = z + (k + t) * K::PV + 8 * (wc * K::NO + y) + g;
-            b.set(0, pb[0]);
-            b.set(1, pb[4 * K::PV]);
-            lin_mma_split<SX, SZ>(o[y], a, b);
+            b[y].set(0, pb[0]);
+            b[y].set(1, pb[4 * K::PV]);
           }
+          lin_mma_split<K::NO, SX, SZ>(o, a, b, K::NO);
         }
       };
       using Yes = std::integral_constant<bool, true>;
@@ -372,14 +403,14 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
         a.set(1, pa[8]);
         a.set(2, pa[4 * K::PA]);
         a.set(3, pa[4 * K::PA + 8]);
+        LinFrag<2, true> b[K::NS];
 #pragma unroll
         for (int y = 0; y < K::NS; ++y) {
-          LinFrag<2, true> b;
           const float* pb = sW + (k + t) * K::PV + 8 * (sn0 + y) + g;
-          b.set(0, pb[0]);
-          b.set(1, pb[4 * K::PV]);
-          lin_mma_split<X, true>(u[y], a, b);
+          b[y].set(0, pb[0]);
+          b[y].set(1, pb[4 * K::PV]);
         }
+        lin_mma_split<K::NS, X, true>(u, a, b, K::NS);
       }
 #pragma unroll
       for (int y = 0; y < K::NS; ++y)
