@@ -12,6 +12,7 @@ is asynchronous on torch's current stream of the tensors' device; the calls can 
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import numpy as np
@@ -38,7 +39,7 @@ def _addresses() -> ctypes.CDLL:
 
 
 fast = _addresses()
-_ROWS = {n: ctypes.c_longlong * (4 * n) for n in (4, 6, 7)}
+_ROWS = {n: (struct.Struct(f"{4 * n}q"), ctypes.c_char * (_HEADS_BYTES * n), _HEADS_BYTES * n) for n in (4, 6, 7)}
 
 
 def _dtypes():
@@ -62,49 +63,72 @@ def _ok(status: int) -> None:
 
 
 def _first(name, t):
-    """Checks of the tensor that the others are held to: its leading sizes."""
-    shape = t.shape
-    if len(shape) not in (3, 4):
+    """The tensor that the others are held to: (dims, B, T, heads, dim, dtype, device number)."""
+    nd = t.dim()
+    if nd == 4:
+        B, T, h, d = t.shape
+    elif nd == 3:
+        T, h, d = t.shape
+        B = 1
+    else:
         raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return shape[:-2]
+    return nd, B, T, h, d, t.dtype, t.get_device()
 
 
-def _heads(name, t, like, shape):
-    """(address, batch, token and head stride) of a tensor of that shape, type and device."""
-    if t.shape != shape or t.dtype is not like.dtype or t.device != like.device:
-        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}; {tuple(shape)} {like.dtype} on {like.device} "
-                         "is wanted")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1 and t.numel():
+def _heads(name, t, like, heads, dim):
+    """(address, batch, token and head stride) of a tensor with the first one's rows, type and device."""
+    nd, B, T, _, _, dtype, device = like
+    if t.dim() != nd:
+        raise ValueError(f"{name} has {t.dim()} dimensions; {nd} are wanted")
+    if nd == 4:
+        b, n, h, e = t.shape
+        x, y, z, w = t.stride()
+    else:
+        n, h, e = t.shape
+        y, z, w = t.stride()
+        b, x = 1, 0
+    if n != T or e != dim or h != heads or b != B or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}; {(B, T, heads, dim)[4 - nd:]} {dtype} on "
+                         f"cuda:{device} is wanted")
+    if w != 1 and e > 1 and t.numel():
         raise ValueError(f"{name} must have contiguous rows")
-    if len(st) == 3:
-        return t.data_ptr(), 0, st[0], st[1]
-    return t.data_ptr(), st[0], st[1], st[2]
+    return t.data_ptr(), x, y, z
 
 
-def _output(name, t, like, shape):
+def _output(name, t, like, heads, dim):
     """The same of an output: tensors whose elements share memory (expanded ones) are refused."""
-    h = _heads(name, t, like, shape)
-    if 0 in h[1:]:
+    row = _heads(name, t, like, heads, dim)
+    if 0 in row[1:]:
         for n, s in zip(t.shape, t.stride()):
             if n > 1 and s == 0:
                 raise ValueError(f"{name} has overlapping elements")
-    return h
+    return row
+
+
+def _fresh(t, nd):
+    """The same of a tensor just made."""
+    if nd == 4:
+        x, y, z, _ = t.stride()
+        return t.data_ptr(), x, y, z
+    y, z, _ = t.stride()
+    return t.data_ptr(), 0, y, z
 
 
 def _rows(*heads):
-    """One array of all of them, and the address of each."""
-    flat = [v for h in heads for v in h]
-    array = _ROWS[len(heads)](*flat)
-    at = ctypes.addressof(array)
-    return array, [at + _HEADS_BYTES * i for i in range(len(heads))]
+    """Memory that holds the pn_heads of all of them, and the address of each."""
+    layout, kind, n = _ROWS[len(heads)]
+    memory = kind()
+    at = ctypes.addressof(memory)
+    layout.pack_into(memory, 0, *[v for row in heads for v in row])
+    return memory, range(at, at + n, _HEADS_BYTES)
 
 
 def _ints(name, t, shape, dtype, device):
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    """Address of a contiguous tensor of integers; device: its number."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{device}")
     return t.data_ptr()
 
 
@@ -112,23 +136,25 @@ def _float32(name, t, shape, device):
     import torch
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on {device}")
+    if t.dtype is not torch.float32 or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape)} on cuda:{device}")
     return t.data_ptr()
 
 
-def _weights(wq, wk, dim, like):
-    """Pointers and type of a norm's weights: float32, or the queries' type."""
+def _weights(wq, wk, dim, device):
+    """Addresses and type of a norm's weights: float32, or the queries' type (which the library checks)."""
+    dtype = wq.dtype
     for name, w in (("wq", wq), ("wk", wk)):
-        if w.shape != (dim,) or not w.is_contiguous() or w.device != like.device or w.dtype is not wq.dtype:
-            raise ValueError(f"{name} must be a contiguous [{dim}] tensor on {like.device}, both weights of one type")
+        if w.shape != (dim,) or not w.is_contiguous() or w.get_device() != device or w.dtype is not dtype:
+            raise ValueError(f"{name} must be a contiguous [{dim}] tensor on cuda:{device}, both weights of one type")
     return wq.data_ptr(), wk.data_ptr(), _dtype("wq", wq)
 
 
 def _stream(device):
+    """torch's current stream of a device (by its number)."""
     import torch
     try:   # torch.cuda.current_stream without its Stream object
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(device)
     except AttributeError:
         return torch.cuda.current_stream(device).cuda_stream
 
@@ -179,31 +205,31 @@ class Rotary:
             pass
 
     @staticmethod
-    def _operands(q, k):
-        """(rows of q, rows of k, k's shape, (dtype, B, T, Hq, Hk, dim))."""
-        lead = _first("q", q)
-        sq, sk = q.shape, k.shape
-        want = lead + (sk[-2] if len(sk) > 1 else 0, sq[-1])
-        B, T = (1, sq[0]) if len(lead) == 1 else lead
-        return _heads("q", q, q, sq), _heads("k", k, q, want), want, (_dtype("q", q), B, T, sq[-2], want[-2], sq[-1])
+    def _operands(q, k, positions):
+        """(what k and the others are held to, key heads, rows of q and of k, address of positions)."""
+        import torch
+        like = nd, B, T, H, d, _, device = _first("q", q)
+        K = k.shape[-2] if k.dim() == nd else 0
+        return (like, K, _heads("q", q, like, H, d), _heads("k", k, like, K, d),
+                _ints("positions", positions, (B, T) if nd == 4 else (T,), torch.int64, device))
 
     @staticmethod
-    def _out(q, k, sk, out):
+    def _out(q, k, like, K, out):
         import torch
+        nd, _, _, H, d, _, _ = like
         if out is None:
             oq, ok = torch.empty_like(q), torch.empty_like(k)
-            return (oq, ok), _heads("q", oq, q, q.shape), _heads("k", ok, q, sk)
+            return (oq, ok), _fresh(oq, nd), _fresh(ok, nd)
         oq, ok = out
-        return (oq, ok), _output("out[0]", oq, q, q.shape), _output("out[1]", ok, q, sk)
+        return (oq, ok), _output("out[0]", oq, like, H, d), _output("out[1]", ok, like, K, d)
 
     def _rotate(self, q, k, positions, out, inverse):
-        import torch
-        hq, hk, sk, shape = self._operands(q, k)
-        device = q.device
-        pos = _ints("positions", positions, q.shape[:-2], torch.int64, device)
-        out, oq, ok = self._out(q, k, sk, out)
+        like, K, hq, hk, pos = self._operands(q, k, positions)
+        _, B, T, H, d, _, device = like
+        out, oq, ok = self._out(q, k, like, K, out)
         keep, at = _rows(hq, hk, oq, ok)
-        _ok(fast.pn_rotary_apply(self.h, *shape, at[0], at[1], pos, inverse, at[2], at[3], _stream(device)))
+        _ok(fast.pn_rotary_apply(self.h, _dtype("q", q), B, T, H, K, d, at[0], at[1], pos, inverse, at[2], at[3],
+                                 _stream(device)))
         return out
 
     def apply(self, q, k, positions, out=None):
@@ -218,32 +244,30 @@ class Rotary:
     def norm_apply(self, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
         """x_j w_j / sqrt(mean(x^2) + eps) of each head vector, then the rotation, in one pass.  The weights are [dim],
         float32 or of the queries' type."""
-        import torch
-        hq, hk, sk, shape = self._operands(q, k)
-        device = q.device
-        pos = _ints("positions", positions, q.shape[:-2], torch.int64, device)
-        w = _weights(wq, wk, shape[-1], q)
-        out, oq, ok = self._out(q, k, sk, out)
+        like, K, hq, hk, pos = self._operands(q, k, positions)
+        _, B, T, H, d, _, device = like
+        w = _weights(wq, wk, d, device)
+        out, oq, ok = self._out(q, k, like, K, out)
         keep, at = _rows(hq, hk, oq, ok)
-        _ok(fast.pn_norm_rotary_apply(self.h, *shape, at[0], at[1], pos, *w, eps, at[2], at[3], _stream(device)))
+        _ok(fast.pn_norm_rotary_apply(self.h, _dtype("q", q), B, T, H, K, d, at[0], at[1], pos, *w, eps, at[2], at[3],
+                                      _stream(device)))
         return out
 
     def norm_backward(self, dq_out, dk_out, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
         """(dq, dk, dwq, dwk) of :meth:`norm_apply`; dwq and dwk are float32 [dim].  ``out`` may be (dq_out, dk_out)."""
         import torch
-        hq, hk, sk, shape = self._operands(q, k)
-        device = q.device
-        gq, gk = _heads("dq_out", dq_out, q, q.shape), _heads("dk_out", dk_out, q, sk)
-        pos = _ints("positions", positions, q.shape[:-2], torch.int64, device)
-        w = _weights(wq, wk, shape[-1], q)
-        out, oq, ok = self._out(q, k, sk, out)
-        dw = torch.empty(2, shape[-1], dtype=torch.float32, device=device)
-        n = lib.pn_norm_rotary_workspace(*shape[1:])
-        keep_w, ws = _workspace(n, device)
+        like, K, hq, hk, pos = self._operands(q, k, positions)
+        _, B, T, H, d, _, device = like
+        gq, gk = _heads("dq_out", dq_out, like, H, d), _heads("dk_out", dk_out, like, K, d)
+        w = _weights(wq, wk, d, device)
+        out, oq, ok = self._out(q, k, like, K, out)
+        dw = torch.empty((2, d), dtype=torch.float32, device=q.device)
+        n = lib.pn_norm_rotary_workspace(B, T, H, K, d)
+        keep_w, ws = _workspace(n, q.device)
         keep, at = _rows(gq, gk, hq, hk, oq, ok)
         at_w = dw.data_ptr()
-        _ok(fast.pn_norm_rotary_backward(self.h, *shape, *at[:4], pos, *w, eps, at[4], at[5], at_w, at_w + 4 * shape[-1], ws,
-                                         n, _stream(device)))
+        _ok(fast.pn_norm_rotary_backward(self.h, _dtype("q", q), B, T, H, K, d, *at[:4], pos, *w, eps, at[4], at[5], at_w,
+                                         at_w + 4 * d, ws, n, _stream(device)))
         return out[0], out[1], dw[0], dw[1]
 
 
@@ -286,25 +310,29 @@ class LinearAttention:
             pass
 
     def _operands(self, q, k, v):
-        """Rows of q, k and v, and the shape of the outputs."""
-        lead = _first("q", q)
-        if q.dtype is not self.dtype:
+        """What the others are held to, and the rows of q, k and v."""
+        like = _first("q", q)
+        if like[5] is not self.dtype:
             raise ValueError(f"q is {q.dtype}; {self.dtype} is wanted")
-        return (_heads("q", q, q, lead + (self.heads, self.dk)), _heads("k", k, q, lead + (self.kv_heads, self.dk)),
-                _heads("v", v, q, lead + (self.kv_heads, self.dv)), lead + (self.heads, self.dv))
+        return (like, _heads("q", q, like, self.heads, self.dk), _heads("k", k, like, self.kv_heads, self.dk),
+                _heads("v", v, like, self.kv_heads, self.dv))
 
-    def _sequences(self, q, cu_seqlens, max_len):
-        """(n_seq, T, cu pointer, max_len) of the rows."""
+    def _sequences(self, like, cu_seqlens, max_len):
+        """(n_seq, T, address of cu_seqlens, max_len) of the rows."""
         import torch
+        nd, B, T, _, _, _, device = like
         if cu_seqlens is None:
-            n, T = (1, q.shape[0]) if q.dim() == 3 else q.shape[:2]
-            return n, T, None, 0
-        if q.dim() != 3:
+            return B, T, None, 0
+        if nd != 3:
             raise ValueError("packed sequences (cu_seqlens) are [tokens, heads, dim]")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [sequences + 1]")
-        return (cu_seqlens.numel() - 1, q.shape[0],
-                _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, q.device), int(max_len or 0))
+        return (cu_seqlens.numel() - 1, T, _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device),
+                int(max_len or 0))
+
+    def _empty(self, q):
+        import torch
+        return torch.empty_like(q) if self.dv == self.dk else q.new_empty(q.shape[:-1] + (self.dv,))
 
     def forward(self, q, k, v, initial_state=None, cu_seqlens=None, max_len: Optional[int] = None, out=None):
         """(o, final state) of whole sequences.
@@ -314,16 +342,18 @@ class LinearAttention:
         written.  ``max_len``: the longest sequence, a hint for the work's split.  States: float32
         [sequences, heads, dk, dv].  ``out``: a tensor for o."""
         import torch
-        hq, hk, hv, so = self._operands(q, k, v)
-        n, T, cu, max_len = self._sequences(q, cu_seqlens, max_len)
-        shape, device = (n, self.heads, self.dk, self.dv), q.device
+        like, hq, hk, hv = self._operands(q, k, v)
+        n, T, cu, max_len = self._sequences(like, cu_seqlens, max_len)
+        shape, device = (n, self.heads, self.dk, self.dv), like[-1]
         s0 = _float32("initial_state", initial_state, shape, device)
-        state = torch.empty(shape, dtype=torch.float32, device=device)
+        state = q.new_empty(shape, dtype=torch.float32) if s0 is None else torch.empty_like(initial_state)
         if out is None:
-            out = torch.empty(so, dtype=q.dtype, device=device)
-        ho = _output("out", out, q, so)
+            out = self._empty(q)
+            ho = _fresh(out, like[0])
+        else:
+            ho = _output("out", out, like, self.heads, self.dv)
         size = lib.pn_linattn_workspace(self.h, 0, n, T, cu is not None, max_len)
-        keep_w, ws = _workspace(size, device)
+        keep_w, ws = _workspace(size, q.device)
         keep, at = _rows(hq, hk, hv, ho)
         _ok(fast.pn_linattn_forward(self.h, n, T, cu, max_len, *at[:3], s0, at[3], state.data_ptr(), ws, size, _stream(device)))
         return out, state
@@ -333,18 +363,19 @@ class LinearAttention:
         """(dq, dk, dv, gradient of the initial state) of :meth:`forward` with the same inputs, from the gradients of o
         and (None: zero) of the final state.  ``grads``: a triple of tensors for dq, dk and dv."""
         import torch
-        hq, hk, hv, so = self._operands(q, k, v)
-        n, T, cu, max_len = self._sequences(q, cu_seqlens, max_len)
-        shape, device = (n, self.heads, self.dk, self.dv), q.device
-        hdo = _heads("do", do, q, so)
+        like, hq, hk, hv = self._operands(q, k, v)
+        n, T, cu, max_len = self._sequences(like, cu_seqlens, max_len)
+        shape, device = (n, self.heads, self.dk, self.dv), like[-1]
+        hdo = _heads("do", do, like, self.heads, self.dv)
         s0 = _float32("initial_state", initial_state, shape, device)
         ds = _float32("dstate", dstate, shape, device)
         if grads is None:
             grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
-        outs = [_output(f"grads[{i}]", g, q, x.shape) for i, (g, x) in enumerate(zip(grads, (q, k, v)))]
-        ds0 = torch.empty(shape, dtype=torch.float32, device=device)
+        sizes = ((self.heads, self.dk), (self.kv_heads, self.dk), (self.kv_heads, self.dv))
+        outs = [_output(f"grads[{i}]", g, like, *size) for i, (g, size) in enumerate(zip(grads, sizes))]
+        ds0 = q.new_empty(shape, dtype=torch.float32)
         size = lib.pn_linattn_workspace(self.h, 1, n, T, cu is not None, max_len)
-        keep_w, ws = _workspace(size, device)
+        keep_w, ws = _workspace(size, q.device)
         keep, at = _rows(hdo, hq, hk, hv, *outs)
         _ok(fast.pn_linattn_backward(self.h, n, T, cu, max_len, *at[:4], s0, ds, *at[4:], ds0.data_ptr(), ws, size,
                                      _stream(device)))
@@ -369,11 +400,13 @@ class LinearAttention:
         import torch
         if q.dim() != 3:
             raise ValueError("q must be [rows, heads, dk]")
-        hq, hk, hv, so = self._operands(q, k, v)
-        rows, device = so[0], q.device
+        like, hq, hk, hv = self._operands(q, k, v)
+        rows, device = like[2], like[-1]
         if out is None:
-            out = torch.empty(so, dtype=q.dtype, device=device)
-        ho = _output("out", out, q, so)
+            out = self._empty(q)
+            ho = _fresh(out, 3)
+        else:
+            ho = _output("out", out, like, self.heads, self.dv)
         if states.dim() != 4:
             raise ValueError("states must be [slots, heads, dk, dv]")
         n = states.shape[0]
@@ -381,13 +414,13 @@ class LinearAttention:
         sl = None if slots is None else _ints("slots", slots, (rows,), torch.int64, device)
         if (wq is None) != (wk is None):
             raise ValueError("wq and wk come together")
-        w = (None, None, PN_F32) if wq is None else _weights(wq, wk, self.dk, q)
+        w = (None, None, PN_F32) if wq is None else _weights(wq, wk, self.dk, device)
         if (rotary is None) != (positions is None):
             raise ValueError("rotary and positions come together")
         turn, pos = None, None
         if rotary is not None:
             turn, pos = rotary.h, _ints("positions", positions, (rows,), torch.int64, device)
         # rows lie at the batch stride
-        keep, at = _rows(*[(h[0], h[2], 0, h[3]) for h in (hq, hk, hv, ho)])
+        keep, at = _rows(*[(p, y, 0, z) for p, _, y, z in (hq, hk, hv, ho)])
         _ok(fast.pn_linattn_step(self.h, rows, *at, st, n, sl, turn, pos, *w, eps, _stream(device)))
         return out
