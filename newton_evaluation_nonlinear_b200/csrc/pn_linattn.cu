@@ -42,9 +42,16 @@ int mma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int d
   return (int)std::max(1LL, std::min(want, max_len / (4 * mma_chunk(da))));
 }
 
+// Columns of c that one CTA of the tensor-core kernel takes: 64 where 128 leave SMs idle (a and b are then read twice, out of
+// L2, which costs less than a second part).
+int tc_columns(const pn_linattn_s* h, int n_seq, int dc) {
+  return dc <= 64 || (long long)n_seq * h->H * ((dc + 63) / 64) <= 148 ? 64 : 128;
+}
+
 // Parts for the tensor-core kernel: a CTA fills its SM, so as many as fit the card beside each other.
-int tc_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int dc) {
-  const long long ctas = (long long)n_seq * h->H * ((dc + 127) / 128);
+int tc_parts(const pn_linattn_s* h, int n_seq, long long max_len, int dc) {
+  const int w = tc_columns(h, n_seq, dc);
+  const long long ctas = (long long)n_seq * h->H * ((dc + w - 1) / w);
   const long long want = 148 / std::max(1LL, ctas);
   return (int)std::max(1LL, std::min(want, max_len / (4 * 64)));
 }
@@ -56,7 +63,7 @@ size_t seg_bytes(const pn_linattn_s* h, int n_seq, long long max_len) {
   int p = 1;
   for (int t = 0; t < 2; ++t) {
     const int da = t ? h->dv : h->dk, dc = t ? h->dk : h->dv;
-    p = std::max(p, std::max(mma_parts(h, n_seq, max_len, da, dc), tc_parts(h, n_seq, max_len, da, dc)));
+    p = std::max(p, std::max(mma_parts(h, n_seq, max_len, da, dc), tc_parts(h, n_seq, max_len, dc)));
   }
   return p > 1 ? align256((size_t)n_seq * h->H * p * h->dk * h->dv * sizeof(float)) : 0;
 }
@@ -137,10 +144,11 @@ bool try_tc(const pn_linattn_s* h, LinPass& P, const LinDecay& G, long long max_
       !encode_operand(&maps.c, P.c, P.dc, P.H / P.c.per, P.T, batch))
     return false;
   P.out_map = !P.out_f32 && encode_operand(&maps.o, LinOperand{P.out, P.out_bs, P.out_ts, P.out_hs, 1}, P.dc, P.H, P.T, batch);
-  P.nseg = tc_parts(h, P.n_seq, max_len, P.da, P.dc);
+  P.nseg = tc_parts(h, P.n_seq, max_len, P.dc);
   using T = __nv_bfloat16;
-  if (P.da <= 64) *e = P.dc <= 64 ? launch_tc<T, 64, 64>(maps, P, G, st) : launch_tc<T, 64, 128>(maps, P, G, st);
-  else *e = P.dc <= 64 ? launch_tc<T, 128, 64>(maps, P, G, st) : launch_tc<T, 128, 128>(maps, P, G, st);
+  const bool narrow = tc_columns(h, P.n_seq, P.dc) == 64;
+  if (P.da <= 64) *e = narrow ? launch_tc<T, 64, 64>(maps, P, G, st) : launch_tc<T, 64, 128>(maps, P, G, st);
+  else *e = narrow ? launch_tc<T, 128, 64>(maps, P, G, st) : launch_tc<T, 128, 128>(maps, P, G, st);
   return true;
 }
 
