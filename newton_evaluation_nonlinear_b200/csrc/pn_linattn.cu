@@ -79,7 +79,7 @@ cudaError_t launch_mma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
       return e;
     lin_mma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), kLinThreads, K::SMEM_BYTES, st>>>(P, G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, C, 0);
+    lin_combine_kernel<<<dim3((P.da * P.dc + 511) / 512, P.n_seq * P.H), 128, 0, st>>>(P, G, C, 0);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if ((e = cudaFuncSetAttribute(lin_mma_kernel<T, C, DA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -127,7 +127,7 @@ cudaError_t launch_tc(const LinMaps& maps, const LinPass& P, const LinDecay& G, 
   if (P.nseg > 1) {
     cudaError_t e = launch_tc_kernel<T, DA, DC, kLinStateOnly>(maps, P, G, P.nseg - 1, st);
     if (e != cudaSuccess) return e;
-    lin_combine_kernel<<<dim3((P.da * P.dc + 255) / 256, P.n_seq * P.H), 256, 0, st>>>(P, G, LinTcCfg<DA, DC>::C, 1);
+    lin_combine_kernel<<<dim3((P.da * P.dc + 511) / 512, P.n_seq * P.H), 128, 0, st>>>(P, G, LinTcCfg<DA, DC>::C, 1);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   return P.out_f32 ? launch_tc_kernel<T, DA, DC, kLinOutF32>(maps, P, G, P.nseg, st)

@@ -453,11 +453,12 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
 // caller's state, in order of the parts.  `chunked`: parts are whole chunks of C in
 // the order of the rows even against time, so that the first part then has the short
 // chunk; else they are rows in the order they are taken.
-__global__ void __launch_bounds__(256) lin_combine_kernel(const __grid_constant__ LinPass P,
+__global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant__ LinPass P,
                                                           const __grid_constant__ LinDecay G, int C, int chunked) {
+  constexpr int kFlight = 8;   // parts read at once
   const int sh = blockIdx.y;
   const int h = sh % P.H, s = sh / P.H;
-  const int e = blockIdx.x * 256 + threadIdx.x;
+  const int e = 4 * (blockIdx.x * 128 + threadIdx.x);   // four neighbours of a state (widths are multiples of 8)
   const int size = P.da * P.dc;
   if (e >= size) return;
   long long start;
@@ -466,16 +467,35 @@ __global__ void __launch_bounds__(256) lin_combine_kernel(const __grid_constant_
   const int nch = (len + C - 1) / C;
   const int seg_len = chunked ? (nch + P.nseg - 1) / P.nseg * C : lin_seg_len(len, P.nseg, C);
   const int first = seg_len - (chunked && P.reverse ? nch * C - len : 0);   // rows of part 0, where others follow it
+  const int rows = chunked ? nch * C : len;
+  const int parts = seg_len > 0 ? min(P.nseg, (rows + seg_len - 1) / seg_len) : 1;   // with rows
   const int i = e / P.dc, j = e % P.dc;
-  float v = P.s_in ? P.s_in[(long long)sh * size + (long long)i * P.s_row + (long long)j * P.s_col] : 0.0f;
-  float* at = P.seg_state + (long long)sh * P.nseg * size + e;
-  at[0] = v;   // the parts read it here: the last one may overwrite the caller's state meanwhile
+  float v[4] = {};
+  if (P.s_in) {
+    const float* in = P.s_in + (long long)sh * size + (long long)i * P.s_row + (long long)j * P.s_col;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = in[(long long)x * P.s_col];
+  }
+  float4* at = reinterpret_cast<float4*>(P.seg_state + (long long)sh * P.nseg * size + e);
+  const long long step = size / 4;
+  at[0] = make_float4(v[0], v[1], v[2], v[3]);   // the parts read it here: the last one may overwrite the caller's state meanwhile
   const float f = lin_pow(G.log2[h], seg_len);
   float f_in = lin_pow(G.log2[h], first - (P.reverse ? 1 : 0));
-  for (int p = 1; p < P.nseg && (long long)p * seg_len < (chunked ? (long long)nch * C : (long long)len); ++p) {
-    v = fmaf(f_in, v, at[(long long)p * size]);
-    at[(long long)p * size] = v;
-    f_in = f;
+  for (int p0 = 1; p0 < parts; p0 += kFlight) {
+    float4 left[kFlight];
+#pragma unroll
+    for (int p = 0; p < kFlight; ++p)
+      if (p0 + p < parts) left[p] = at[(p0 + p) * step];
+#pragma unroll
+    for (int p = 0; p < kFlight; ++p) {
+      if (p0 + p >= parts) break;
+      v[0] = fmaf(f_in, v[0], left[p].x);
+      v[1] = fmaf(f_in, v[1], left[p].y);
+      v[2] = fmaf(f_in, v[2], left[p].z);
+      v[3] = fmaf(f_in, v[3], left[p].w);
+      at[(p0 + p) * step] = make_float4(v[0], v[1], v[2], v[3]);
+      f_in = f;
+    }
   }
 }
 
