@@ -500,29 +500,35 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
 }
 
 // dst = sum of the partial gradients [rows][H][d] of each group of heads, in the
-// order of the heads; rows of no sequence are left as they are.
+// order of the heads, four neighbours to a thread; rows of no sequence are left as
+// they are.  A block takes whole rows of K heads.
 template <typename T>
 __global__ void __launch_bounds__(256) lin_group_sum_kernel(const float* __restrict__ part, long long rows, int H, int G,
                                                             int d, T* dst, long long bs, long long ts, long long hs,
-                                                            long long tokens, const int* cu, int n_seq) {
-  const int K = H / G;
-  const long long n = rows * K * d;
+                                                            long long tokens, const int* cu, int n_seq, int vec) {
+  const int K = H / G, quads = K * d / 4;
   long long lo = 0, hi = rows;
   if (cu) {
-    lo = cu[0];
-    hi = cu[n_seq];
+    lo = max(0LL, (long long)cu[0]);
+    hi = min(rows, (long long)cu[n_seq]);
   }
-  for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < n; e += (long long)gridDim.x * 256) {
-    const int j = (int)(e % d);
-    const long long rk = e / d;
-    const int k = (int)(rk % K);
-    const long long r = rk / K;
-    if (r < lo || r >= hi) continue;
-    const float* p = part + (r * H + (long long)k * G) * d + j;
-    float v = 0.0f;
-    for (int g = 0; g < G; ++g) v += p[(long long)g * d];
+  for (long long r = lo + blockIdx.x; r < hi; r += gridDim.x) {
     const long long b = r / tokens, t = r - b * tokens;
-    dst[b * bs + t * ts + k * hs + j] = from_f<T>(v);
+    T* out = dst + b * bs + t * ts;
+    for (int e = threadIdx.x; e < quads; e += 256) {
+      const int k = 4 * e / d, j = 4 * e - k * d;
+      const float4* p = reinterpret_cast<const float4*>(part + (r * H + (long long)k * G) * d + j);
+      float v[4] = {};
+#pragma unroll 4
+      for (int g = 0; g < G; ++g) {
+        const float4 x = p[(long long)g * (d / 4)];
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
+      }
+      lin_store4<T>(out + k * hs + j, vec, v);
+    }
   }
 }
 

@@ -540,11 +540,20 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
           }
           const int c0 = DC == 128 ? 32 * w + 16 * g : 16 * w;   // first column of c
           if constexpr (WHAT == kLinOutF32) {
-            float* o = (float*)P.out + at + (start + (long long)chunk_of(m) * C) * P.out_ts + c0 + fr;
+            float* o = (float*)P.out + at + (start + (long long)chunk_of(m) * C + r0 + fc) * P.out_ts + c0 + fr;
+            const int left = n - r0 - fc;   // rows from this thread's first on
+            const bool on0 = dc0 + c0 + fr < P.dc, on1 = dc0 + c0 + fr + 8 < P.dc;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int r = r0 + (e >> 2) * 8 + fc + (e & 1), c = (e & 2) * 4;
-              if (r < n && dc0 + c0 + fr + c < P.dc) o[(long long)r * P.out_ts + c] = x[e];
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float* oe = e ? o + P.out_ts : o;
+                if (8 * k + e < left) {
+                  if (on0) oe[0] = x[4 * k + e];
+                  if (on1) oe[8] = x[4 * k + e + 2];
+                }
+              }
+              o += 8 * P.out_ts;
             }
           } else {
             // transposed: row r0 + 8 (k + (mi >> 1)) + mr, 8 columns from c0 + 8 (mi & 1)
