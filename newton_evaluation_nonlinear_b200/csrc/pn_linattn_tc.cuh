@@ -46,7 +46,7 @@
 
 #include <type_traits>
 
-#include "pn_iter_diag_tc.cuh"
+#include "pn_wide_gemm.cuh"
 #include "pn_linattn.cuh"
 
 namespace pn {
@@ -225,16 +225,17 @@ struct LinTcCfg {
   static constexpr int SB_BYTES = DC * DA * 2;             // S~^T
   static constexpr int P_BYTES = C * C * 2;                // P~
   static constexpr int NP = 3;                             // pieces of c'
-  static constexpr int O_BYTES = C * DC * 2;               // outputs on their way
+  static constexpr int O_BYTES = C * DC * 2;               // outputs on their way, twice where there is room
+  static constexpr int NOUT = DA == 128 && DC == 128 ? 1 : 2;
   static constexpr bool TS = DC == 128;                    // the pieces lie in TMEM
   static constexpr int CP_BYTES = TS ? 0 : 2 * NP * C_BYTES;   // (twice, as in TMEM)
-  static constexpr int FIXED = SB_BYTES + 2 * P_BYTES + CP_BYTES + O_BYTES;
+  static constexpr int FIXED = SB_BYTES + 2 * P_BYTES + CP_BYTES + NOUT * O_BYTES;
   static constexpr int NSTAGE = (220 * 1024 - FIXED) / STAGE < 4 ? (220 * 1024 - FIXED) / STAGE : 4;
   static constexpr int OFF_SB = NSTAGE * STAGE;
   static constexpr int OFF_P = OFF_SB + SB_BYTES;
   static constexpr int OFF_CP = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_O = OFF_CP + CP_BYTES;
-  static constexpr int SMEM_BYTES = OFF_O + O_BYTES + 1024;   // + alignment slack
+  static constexpr int SMEM_BYTES = OFF_O + NOUT * O_BYTES + 1024;   // + alignment slack
   static constexpr int COL_U = 0, COL_P = DA, COL_O = DA + 64;   // outputs twice: two chunks', or O1 and O2 of one
   static constexpr int COL_CP = DA + 192;                  // twice 32 columns a piece
   static constexpr int TCOLS = 512;
@@ -509,10 +510,13 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       const int fr = lane >> 2, fc = 2 * (lane & 3), mr = lane & 7, mi = lane >> 3;
       const long long at = (P.cu ? 0 : s * P.out_bs) + (long long)h * P.out_hs + dc0;
       const bool wide = P.out_map || (((uintptr_t)P.out | (uintptr_t)(2 * P.out_bs) | (uintptr_t)(2 * P.out_ts) | (uintptr_t)(2 * P.out_hs)) & 15u) == 0;
-      unsigned char* stage = base + K::OFF_O;
       for (int m = 0; m < M; ++m) {
+        unsigned char* stage = base + K::OFF_O + (K::NOUT == 2 ? (m & 1) * K::O_BYTES : 0);
         const bool ok = lin_wait(&bar_oacc[m & 1], (unsigned)(m >> 1) & 1u, &s_abort);
-        if (t == 0) bulk_wait_read();   // the copy before has read the staged outputs
+        if (t == 0) {   // the copy that last read this memory is done with it
+          if (K::NOUT == 2) bulk_wait_read_but1();
+          else bulk_wait_read();
+        }
         if (!named_barrier_and(1, 128, ok)) break;   // one decision; and the staged outputs before these are gone
         tc_fence_after();
         const int n = rows_of(m);
