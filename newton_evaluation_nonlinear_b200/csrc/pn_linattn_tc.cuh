@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
   constexpr bool STATE_ONLY = WHAT == kLinStateOnly;
   extern __shared__ __align__(1024) unsigned char smem_lt[];
   unsigned char* base = smem_lt + ((1024u - (smem_addr(smem_lt) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_pacc, bar_p[2], bar_s, bar_u, bar_ur, bar_o1, bar_cp[2], bar_cpf[2], bar_zero, bar_oacc[2], bar_o[2], bar_done[3];
+  __shared__ __align__(8) uint64_t bar_full[NS], bar_empty[NS], bar_pacc, bar_p[2], bar_s, bar_u, bar_ur, bar_o1, bar_cp[2], bar_cpf[2], bar_zero, bar_init, bar_oacc[2], bar_o[2], bar_done[3];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_loaded;
@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     mbar_init(&bar_s, 8u);
     mbar_init(&bar_u, 1u);
     mbar_init(&bar_ur, 8u);
+    mbar_init(&bar_init, 8u);
     mbar_init(&bar_zero, 8u);   // c is zero behind the last row (once, for the one short chunk there may be)
     mbar_init(&bar_o1, 1u);
     for (int i = 0; i < 2; ++i) {
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
         const int bz = P.cu ? 0 : s;
         for (int m = 0; m < M; ++m) {
           const int st = m % NS;
+          if (m == 1 && !lin_wait(&bar_init, 0u, &s_abort)) break;   // the state came in by way of the other stages
           if (m >= NS && !lin_wait(&bar_empty[st], (unsigned)(m / NS - 1) & 1u, &s_abort)) break;
           const int row = (int)start + chunk_of(m) * C;
           mbar_arrive_expect_tx(&bar_full[st], (unsigned)(STATE_ONLY ? K::STAGE - K::A_BYTES : K::STAGE));
@@ -636,24 +638,85 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       dj = P.s_col;
       if (P.reverse && len > 0) f_out = lin_pow(l2, 1);   // against time the first state's gradient still decays by the first row
     }
-    // element e of block (b, q): column c_of(b, e) of c, column d_of(q, e) of a and b
-    auto c_of = [&](int b, int e) { return (DC == 128 ? 32 * w + 16 * b : 16 * w) + fr + (e & 2) * 4; };
-    auto d_of = [&](int q, int e) { return half + 32 * q + (e >> 2) * 8 + fc + (e & 1); };
+    // States go in and out by way of stages that hold no chunk then (the second and third before they do; those of the two
+    // chunks before the last), four neighbours at a time in the order they lie in memory: as fragments, straight, they were
+    // 64 loads of single values in code that runs once, which took 18 us.  Each half of the columns has a stage of its own,
+    // [c][DH] with d moved by 8 (c & 3) places, so that a fragment's pairs lie in different banks.
+    constexpr int DH = DA / 2;
+    static_assert(NS >= 3 && DC * DH * 4 <= K::STAGE, "a stage holds half of a state");
+    const int hi_half = half ? 1 : 0, tw = (warp & 3) * 32 + lane;
+    auto stage_of = [&](int i) { return reinterpret_cast<float*>(base + i * K::STAGE); };
+    // copy f times the state at g (strides gd, gc; one of them is 1) into (or out of) memory x
+    auto carry = [&](auto out, float* x, const float* g, long long gd, long long gc, float f) {
+      constexpr bool kOut = decltype(out)::value;
+      if (gc == 1) {   // c is contiguous: 4 of c times 8 of d to a warp
+#pragma unroll 4
+        for (int i = tw; i < DC * DH / 4; i += 128) {
+          const int c = 4 * ((i & 3) + 4 * (i / (4 * DH))), d = (i >> 2) % DH;
+          if (dc0 + c >= P.dc || half + d >= P.da) {
+            if (!kOut)
+              for (int u = 0; u < 4; ++u) x[(c + u) * DH + (d ^ (8 * u))] = 0.0f;
+            continue;
+          }
+          float4* at = reinterpret_cast<float4*>(const_cast<float*>(g) + (half + d) * gd + dc0 + c);
+          float4 v;
+          if (kOut) {
+            v = make_float4(f * x[c * DH + d], f * x[(c + 1) * DH + (d ^ 8)], f * x[(c + 2) * DH + (d ^ 16)],
+                            f * x[(c + 3) * DH + (d ^ 24)]);
+            *at = v;
+          } else {
+            v = *at;
+            x[c * DH + d] = f * v.x;
+            x[(c + 1) * DH + (d ^ 8)] = f * v.y;
+            x[(c + 2) * DH + (d ^ 16)] = f * v.z;
+            x[(c + 3) * DH + (d ^ 24)] = f * v.w;
+          }
+        }
+      } else {         // d is
+#pragma unroll 4
+        for (int i = tw; i < DC * DH / 4; i += 128) {
+          const int c = i / (DH / 4), d = 4 * (i % (DH / 4));
+          float4* here = reinterpret_cast<float4*>(x + c * DH + (d ^ (8 * (c & 3))));
+          if (dc0 + c >= P.dc || half + d >= P.da) {
+            if (!kOut) *here = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            continue;
+          }
+          float4* at = reinterpret_cast<float4*>(const_cast<float*>(g) + half + d + (dc0 + c) * gc);
+          float4 v = kOut ? *here : *at;
+          v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+          *(kOut ? at : here) = v;
+        }
+      }
+    };
+    // pair (e, e + 1) of block (b, q): row c, column 32 q + 8 (e >> 2) + fc of the half
+    auto pair_at = [&](float* x, int b, int q, int e) {
+      const int c = (DC == 128 ? 32 * w + 16 * b : 16 * w) + fr + (e & 2) * 4;
+      return reinterpret_cast<float2*>(x + c * DH + 32 * q + ((8 * (e >> 2)) ^ (8 * (fr & 3))) + fc);
+    };
     // Against time the first chunk's rows (a short chunk, or the last row undecayed) see the state this much earlier than
     // those of a whole one, for which the row factors and P~ are made: it enters that much larger, and decays as over a
     // whole chunk.
     const int early = P.reverse && !two && M > 0 && !STATE_ONLY ? C - rows_of(0) + e0 : 0;
     const float lead = frame * exp2f(-l2 * (float)early);
-    float S[NB][NQ][16];
+    float S[NB][NQ][16] = {};
+    if (src) {
+      float* x = stage_of(1 + hi_half);
+      carry(std::false_type{}, x, src, sd, sj, lead);
+      named_barrier(2 + hi_half, 128);   // (nothing waited for yet: every warp comes here)
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int q = 0; q < NQ; ++q)
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int c = dc0 + c_of(b, e), d = d_of(q, e);
-          S[b][q][e] = (src && c < P.dc && d < P.da) ? lead * src[d * sd + c * sj] : 0.0f;
-        }
+          for (int e = 0; e < 16; e += 2) {
+            const float2 v = *pair_at(x, b, q, e);
+            S[b][q][e] = v.x;
+            S[b][q][e + 1] = v.y;
+          }
+      fence_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar_init);
     if (!two) f_out *= exp2f(-l2 * R);
     if (STATE_ONLY) f_out = 1.0f;
     const float f_full = lin_pow(l2, C);
@@ -711,16 +774,16 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_s);
     }
-    if (dst && ok) {
+    if (dst) {   // (the same in every thread)
+      float* x = stage_of(M == 0 ? 1 + hi_half : (M + hi_half) % NS);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = dc0 + c_of(b, e), d = d_of(q, e);
-            if (c < P.dc && d < P.da) dst[d * dd + c * dj] = f_out * S[b][q][e];
-          }
+          for (int e = 0; e < 16; e += 2)
+            if (ok) *pair_at(x, b, q, e) = make_float2(S[b][q][e], S[b][q][e + 1]);
+      if (named_barrier_and(2 + hi_half, 128, ok)) carry(std::true_type{}, x, dst, dd, dj, f_out);
     }
   } else {
     regs_give<56>();
