@@ -164,6 +164,54 @@ __device__ __forceinline__ void tmem_st_frag4(uint32_t a, const uint32_t (&r)[4]
                : "memory");
 }
 
+// Copies f times DH x DC values of a state between global memory g (strides gd, gc; one of them is 1; nd x nc values are
+// there, the others count as zero) and shared memory x, [c][DH] with d moved by 8 (c & 3) places; 128 threads.  A function of
+// its own: it runs once, and inlined it lay between the loops, which an instruction cache holds with little to spare (the
+// same loops took 72 or 87 us at 4 x 37 heads x 4096 rows of width 64, by what lay between them).
+template <int DC, int DH, bool OUT>
+__device__ __noinline__ void lin_carry(float* x, const float* g, long long gd, long long gc, float f, int nd, int nc, int tw) {
+  constexpr int kEach = DC * DH / 512, kBatch = kEach < 8 ? kEach : 8;   // groups of four of a thread; on their way at once
+  const bool along_c = gc == 1;   // four of c (times 8 of d to a warp), or four of d
+#pragma unroll 1
+  for (int i0 = tw; i0 < 128 * kEach; i0 += 128 * kBatch) {
+    float4 v[kBatch];
+    auto place = [&](int u, int& c, int& d) {
+      const int i = i0 + 128 * u;
+      c = along_c ? 4 * ((i & 3) + 4 * (i / (4 * DH))) : i / (DH / 4);
+      d = along_c ? (i >> 2) % DH : 4 * (i % (DH / 4));
+      return c < nc && d < nd;
+    };
+    auto memory = [&](int c, int d) { return reinterpret_cast<float4*>(const_cast<float*>(g) + d * gd + c * gc); };
+    auto stage = [&](float4& y, int c, int d, bool store) {
+      if (along_c) {
+        float* z[4] = {x + c * DH + d, x + (c + 1) * DH + (d ^ 8), x + (c + 2) * DH + (d ^ 16), x + (c + 3) * DH + (d ^ 24)};
+        if (store) *z[0] = y.x, *z[1] = y.y, *z[2] = y.z, *z[3] = y.w;
+        else y = make_float4(*z[0], *z[1], *z[2], *z[3]);
+      } else {
+        float4* z = reinterpret_cast<float4*>(x + c * DH + (d ^ (8 * (c & 3))));
+        if (store) *z = y;
+        else y = *z;
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      int c, d;
+      const bool on = place(u, c, d);
+      v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (OUT) stage(v[u], c, d, false);
+      else if (on) v[u] = *memory(c, d);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      int c, d;
+      const bool on = place(u, c, d);
+      v[u] = make_float4(f * v[u].x, f * v[u].y, f * v[u].z, f * v[u].w);
+      if (!OUT) stage(v[u], c, d, true);
+      else if (on) *memory(c, d) = v[u];
+    }
+  }
+}
+
 template <int N> __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -646,47 +694,8 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     static_assert(NS >= 3 && DC * DH * 4 <= K::STAGE, "a stage holds half of a state");
     const int hi_half = half ? 1 : 0, tw = (warp & 3) * 32 + lane;
     auto stage_of = [&](int i) { return reinterpret_cast<float*>(base + i * K::STAGE); };
-    // copy f times the state at g (strides gd, gc; one of them is 1) into (or out of) memory x
     auto carry = [&](auto out, float* x, const float* g, long long gd, long long gc, float f) {
-      constexpr bool kOut = decltype(out)::value;
-      if (gc == 1) {   // c is contiguous: 4 of c times 8 of d to a warp
-#pragma unroll 4
-        for (int i = tw; i < DC * DH / 4; i += 128) {
-          const int c = 4 * ((i & 3) + 4 * (i / (4 * DH))), d = (i >> 2) % DH;
-          if (dc0 + c >= P.dc || half + d >= P.da) {
-            if (!kOut)
-              for (int u = 0; u < 4; ++u) x[(c + u) * DH + (d ^ (8 * u))] = 0.0f;
-            continue;
-          }
-          float4* at = reinterpret_cast<float4*>(const_cast<float*>(g) + (half + d) * gd + dc0 + c);
-          float4 v;
-          if (kOut) {
-            v = make_float4(f * x[c * DH + d], f * x[(c + 1) * DH + (d ^ 8)], f * x[(c + 2) * DH + (d ^ 16)],
-                            f * x[(c + 3) * DH + (d ^ 24)]);
-            *at = v;
-          } else {
-            v = *at;
-            x[c * DH + d] = f * v.x;
-            x[(c + 1) * DH + (d ^ 8)] = f * v.y;
-            x[(c + 2) * DH + (d ^ 16)] = f * v.z;
-            x[(c + 3) * DH + (d ^ 24)] = f * v.w;
-          }
-        }
-      } else {         // d is
-#pragma unroll 4
-        for (int i = tw; i < DC * DH / 4; i += 128) {
-          const int c = i / (DH / 4), d = 4 * (i % (DH / 4));
-          float4* here = reinterpret_cast<float4*>(x + c * DH + (d ^ (8 * (c & 3))));
-          if (dc0 + c >= P.dc || half + d >= P.da) {
-            if (!kOut) *here = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            continue;
-          }
-          float4* at = reinterpret_cast<float4*>(const_cast<float*>(g) + half + d + (dc0 + c) * gc);
-          float4 v = kOut ? *here : *at;
-          v = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
-          *(kOut ? at : here) = v;
-        }
-      }
+      lin_carry<DC, DH, decltype(out)::value>(x, g + half * gd + dc0 * gc, gd, gc, f, P.da - half, P.dc - dc0, tw);
     };
     // pair (e, e + 1) of block (b, q): row c, column 32 q + 8 (e >> 2) + fc of the half
     auto pair_at = [&](float* x, int b, int q, int e) {
