@@ -212,6 +212,27 @@ __device__ __noinline__ void lin_carry(float* x, const float* g, long long gd, l
   }
 }
 
+// The n staged rows of outputs (boxes of 64 columns, 128-byte swizzled) to global memory, 16 bytes a thread where `wide`;
+// nc columns are there; 128 threads.  Short chunks and outputs that TMA cannot store.
+template <typename T, int DC>
+__device__ __noinline__ void lin_rows_out(T* out, const unsigned char* stage, long long ts, int n, int nc, bool wide, int t) {
+#pragma unroll 1
+  for (int e = t; e < 64 * DC / 8; e += 128) {
+    const int r = e / (DC / 8), ch = e % (DC / 8);
+    if (r >= n || 8 * ch >= nc) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + (ch >> 3) * (64 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+    T* o = out + r * ts + 8 * ch;
+    if (wide) {
+      *reinterpret_cast<uint4*>(o) = v;
+    } else {
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+      unsigned short* o16 = reinterpret_cast<unsigned short*>(o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o16[i] = (unsigned short)(u[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
 template <int N> __device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -633,22 +654,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
           }
         } else if (WHAT == kLinOut) {
           named_barrier(1, 128);
-          // 16 bytes a thread, a row's neighbours side by side
-#pragma unroll 1
-          for (int e = t; e < C * DC / 8; e += 128) {
-            const int r = e / (DC / 8), ch = e % (DC / 8);
-            if (r >= n || dc0 + 8 * ch >= P.dc) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + (ch >> 3) * K::SUB + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
-            T* o = out + r * P.out_ts + 8 * ch;
-            if (wide) {
-              *reinterpret_cast<uint4*>(o) = v;
-            } else {
-              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-              unsigned short* o16 = reinterpret_cast<unsigned short*>(o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o16[i] = (unsigned short)(u[i >> 1] >> (16 * (i & 1)));
-            }
-          }
+          lin_rows_out<T, DC>(out, stage, P.out_ts, n, P.dc - dc0, wide, t);
         }
       }
       if (t == 0) bulk_wait_all();
