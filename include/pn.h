@@ -438,10 +438,13 @@ PN_API pn_status pn_norm_rotary_backward(pn_rotary r, int dtype, int B, int T, i
  * and value head h / (H / Hkv),
  *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T     (dk x dv, float32)
  *   o_t = scale q_t S_t.
- * q, k, v and o are of one type (PN_F32, PN_BF16, PN_F16); states are float32.  An infinite or NaN
- * input makes outputs of its sequence and head undefined from up to 127 rows before it (whole chunks
- * are multiplied at once); other sequences, padding rows and rows behind the last one never
- * take part. */
+ * q, k, v and o are of one type (PN_F32, PN_BF16, PN_F16); states are float32, and so are all sums.
+ * Prompts of PN_BF16 with dk <= 128 (and gradients, dv too) and rows that TMA can read (16-byte aligned,
+ * strides above zero) run on tcgen05: the state before a chunk of 64 rows and the weights between its rows
+ * are rounded to bfloat16, once each, for the outputs.  All else runs on the TF32 tensor cores in split form, with float32's
+ * accuracy.  An infinite or NaN input makes outputs of its sequence and head undefined from up to 63 rows
+ * before it (whole chunks are multiplied at once; so do products q.k beyond 2^86); other sequences, padding
+ * rows and rows behind the last one never take part. */
 typedef struct pn_linattn_s* pn_linattn;
 
 /*   H, Hkv     query heads (<= 256), key and value heads (Hkv divides H)

@@ -447,6 +447,129 @@ def test_step_padding_and_repeated_slots():
     assert att.step(q[:0], k[:0], v[:0], states).shape == (0, H, d)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_linear_offsets_are_clamped(dtype):
+    """Offsets outside the buffer are cut to it, a decreasing one makes an empty sequence: nothing else is read or written."""
+    T, H, d = 200, 2, 64
+    att = pn.LinearAttention(H, H, d, d, decays(H), dtype=dtype)
+    q, k, v = (rnd(i, T, H, d, dtype=dtype).cuda() for i in (1, 2, 3))
+    s0 = rnd(4, 3, H, d, d).cuda()
+
+    def run(cu):
+        out = torch.full((T, H, d), 7.0, dtype=dtype, device="cuda")
+        o, S = att.forward(q, k, v, initial_state=s0, cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), max_len=T, out=out)
+        return o, S
+
+    for bad, good in (([-5, 90, 90, 1000000], [0, 90, 90, T]), ([0, 120, 60, 60], [0, 120, 120, 120]),
+                      ([150, 2 ** 31 - 1, 40, 40], [150, T, T, T])):
+        for a, b in zip(run(bad), run(good)):
+            assert torch.equal(a, b), bad
+    pn.LinearAttention.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_many_sequences(dtype):
+    """More sequences than are taken by length, most of them of one to three rows."""
+    n, H, d = 600, 1, 16
+    lens = [(7 * i) % 4 for i in range(n)]
+    lens[311] = 140
+    att = pn.LinearAttention(H, H, d, d, [-0.05], dtype=dtype)
+    T = sum(lens)
+    q, k, v = (rnd(i, T, H, d, dtype=dtype) for i in (1, 2, 3))
+    s0 = rnd(4, n, H, d, d)
+    cu = torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32)
+    o, S = att.forward(q.cuda(), k.cuda(), v.cuda(), initial_state=s0.cuda(), cu_seqlens=cu.cuda())   # no max_len
+    g = torch.tensor([-0.05])
+    for i in (0, 1, 2, 3, 310, 311, 312, n - 1):
+        r = slice(int(cu[i]), int(cu[i + 1]))
+        wo, wS = lo.linear(q[r], k[r], v[r], g, d ** -0.5, s0[i])
+        Ao, AS = lo.linear(q[r].double().abs(), k[r].double().abs(), v[r].double().abs(), g, d ** -0.5, s0[i].abs())
+        check(f"o[{i}]", o[r], wo, half_step(dtype) * wo.abs() + (mixed(dtype) + 2.0 ** -17) * Ao)
+        check(f"S[{i}]", S[i], wS, 2.0 ** -17 * AS)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_linear_long(dtype):
+    """A sequence of many parts.  Its sums have 2^13 terms where nothing is forgotten: 2^-15 A in place of 2^-17 A (errors of
+    float32 sums grow with the square root of the terms, 2^2 for 2^4 times as many; the powers' by the exponent's size, which
+    the decay keeps within the same 20 steps)."""
+    T, H, d = 9001, 2, 32
+    g = torch.tensor([0.0, -0.002])
+    att = pn.LinearAttention(H, 1, d, d, g, dtype=dtype)
+    q, k, v = rnd(1, T, H, d, dtype=dtype), rnd(2, T, 1, d, dtype=dtype), rnd(3, T, 1, d, dtype=dtype)
+    do = rnd(4, T, H, d, dtype=dtype)
+    o, S = att.forward(q[None].cuda(), k[None].cuda(), v[None].cuda())
+    grads = att.backward(do[None].cuda(), q[None].cuda(), k[None].cuda(), v[None].cuda())
+    wo, wS = lo.linear(q, k, v, g, d ** -0.5)
+    want = lo.linear_gradient(do, q, k, v, g, d ** -0.5)
+    mag = [x.double().abs() for x in (q, k, v)]
+    Ao, AS = lo.linear(*mag, g, d ** -0.5)
+    A = lo.linear_gradient(do.double().abs(), *mag, g, d ** -0.5)
+    u, c = half_step(dtype), 2.0 ** -15
+    check("o", o[0], wo, u * wo.abs() + (mixed(dtype) + c) * Ao)
+    check("S", S[0], wS, c * AS)
+    for name, x, w, y in zip(("dq", "dk", "dv"), grads, want, A):
+        check(name, x[0], w, u * w.abs() + (mixed(dtype) + c) * y)
+    check("ds0", grads[3][0], want[3], c * A[3])
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose element offsets, and states whose slots, pass 2^31."""
+    far = 1 << 30
+    base = torch.empty(3 * far + 1024, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(base, (4, 2, 64), (far - 64, 64, 1))   # token 3 lies at element 3 2^30 - 192
+    src = rnd(1, 4, 2, 64, dtype=torch.bfloat16)
+    x.copy_(src)
+    pos = torch.arange(4, device="cuda")
+    near = src.cuda()
+    r, att = pn.Rotary(64), pn.LinearAttention(2, 2, 64, 64, [-0.1, 0.0], dtype=torch.bfloat16)
+    w = torch.ones(64, device="cuda")
+    for a, b in zip(r.norm_apply(x, x, pos, w, w), r.norm_apply(near, near, pos, w, w)):
+        assert torch.equal(a, b)
+    for a, b in zip(att.forward(x[None], x[None], x[None]), att.forward(near[None], near[None], near[None])):
+        assert torch.equal(a, b)
+    half = pn.LinearAttention(2, 2, 64, 64, [-0.1, 0.0], dtype=torch.float16)   # the other kernel
+    xh, nh = x.view(torch.float16), near.view(torch.float16)
+    for a, b in zip(half.forward(xh[None], xh[None], xh[None]), half.forward(nh[None], nh[None], nh[None])):
+        assert torch.equal(a.view(torch.int16) if a.dtype == torch.float16 else a.view(torch.int32),
+                           b.view(torch.int16) if b.dtype == torch.float16 else b.view(torch.int32))
+    del base, x, xh
+    one = pn.LinearAttention(1, 1, 256, 256, [-0.1])
+    states = torch.zeros(33000, 1, 256, 256, device="cuda")   # 2^31 elements at slot 32768
+    q = rnd(2, 1, 1, 256).cuda()
+    o = one.step(q, q, q, states, slots=torch.tensor([32999], device="cuda"))
+    small = torch.zeros(1, 1, 256, 256, device="cuda")
+    assert torch.equal(o, one.step(q, q, q, small)) and torch.equal(states[32999], small[0])
+    assert float(states[:32999].abs().amax()) == 0
+
+
+def test_one_handle_on_two_streams():
+    """Handles hold nothing that a call changes: two streams at once give what each gives alone."""
+    T, H, d = 2000, 4, 64
+    att = pn.LinearAttention(H, 2, d, d, decays(H), dtype=torch.bfloat16)
+    r = pn.Rotary(d)
+    w, pos = torch.ones(d, device="cuda"), torch.arange(T, device="cuda")
+    ins = [(rnd(i, T, H, d, dtype=torch.bfloat16).cuda(), rnd(i + 9, T, 2, d, dtype=torch.bfloat16).cuda()) for i in range(2)]
+
+    def layer(q, k):
+        nq, nk = r.norm_apply(q, k, pos, w, w)
+        o, S = att.forward(nq[None], nk[None], k[None])
+        return (o, S, *att.backward(o, nq[None], nk[None], k[None], dstate=S))
+
+    want = [layer(*x) for x in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = layer(*ins[i])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
 def test_linear_refusals():
     att = pn.LinearAttention(4, 2, 64, 32, [-0.1] * 4)
     q, k, v = torch.zeros(2, 5, 4, 64).cuda(), torch.zeros(2, 5, 2, 64).cuda(), torch.zeros(2, 5, 2, 32).cuda()
