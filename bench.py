@@ -101,9 +101,12 @@ def peaks():
 
 
 def kernel_source_sha() -> str:
-    """Hash of the device code: the kernel headers and the per-cell kernel units (host code excluded)."""
+    """Hash of the iteration's device code: its kernel headers and the per-cell kernel units (host code excluded, and the
+    sequence-layer operators, which none of it includes)."""
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
+        if name.startswith(("pn_seq", "pn_linattn", "pn_heads")):
+            continue
         if name.endswith(".cuh") or (name.startswith("pn_k_") and name.endswith(".cu")):
             with open(os.path.join(CSRC, name), "rb") as f:
                 h.update(f.read())
