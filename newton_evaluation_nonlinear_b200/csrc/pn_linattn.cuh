@@ -178,7 +178,7 @@ __device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4,
 // S is summed in float32 registers (the tensor cores truncate) and copied to
 // shared memory for the outputs.  What it is for is float32, which the tcgen05 kernel
 // does not take: 4 x 16 heads x 4096 rows of width 64 took 616 us by FP32 FMA with
-// 4 x 4 values a thread, which shared memory bounds, and take 325 us so.
+// 4 x 4 values a thread, which shared memory bounds, and take 320 us so.
 // STATE_ONLY leaves out the outputs: what the part adds to the state, from zero.
 template <typename T, int C, int DA, bool STATE_ONLY>
 __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_kernel(const __grid_constant__ LinPass P,
@@ -296,6 +296,20 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
       if (!STATE_ONLY) *reinterpret_cast<float4*>(sC + i * K::PV + j) = make_float4(v[0], v[1], v[2], v[3]);
       const float f = i < n ? P.alpha * sL[n - 1 - i] : 0.0f;
       *reinterpret_cast<float4*>(sW + i * K::PV + j) = make_float4(f * v[0], f * v[1], f * v[2], f * v[3]);
+    }
+    // The next chunk's rows on their way to L2 meanwhile, a line of 128 bytes to a thread: one CTA an SM, as at widths above
+    // 64, has little else in flight (4 x 16 heads x 4096 float16 rows of width 128 960 -> 829 us; float32 892 -> 877, of
+    // width 64 326 -> 320; only a few long heads of width 256 lose, 156 -> 160).
+    if (r0 + C < hi) {
+      const int m = min(C, hi - r0 - C);
+      constexpr int kA = (DA * (int)sizeof(T) + 127) / 128, kV = kLinDC * (int)sizeof(T) / 128;
+      for (int e = tid; e < m * (2 * kA + kV); e += kLinThreads) {
+        const int i = C + e % m, l = e / m;   // row from r0 on, line: a's, b's, c's
+        const int at = 128 / (int)sizeof(T) * (l < kA ? l : l < 2 * kA ? l - kA : l - 2 * kA);
+        const long long r = row_of(i);
+        const T* p = l < kA ? ap + r * P.a.ts : l < 2 * kA ? bp + r * P.b.ts : cp + r * P.c.ts + dc0;
+        if (at < (l < 2 * kA ? da : dc - dc0) && !(STATE_ONLY && l < kA)) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at));
+      }
     }
     __syncthreads();
 
