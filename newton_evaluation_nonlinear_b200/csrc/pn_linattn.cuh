@@ -153,23 +153,44 @@ struct LinFrag {
     }
   }
 };
-// Their products: hi hi + hi lo + lo hi (22 bits of each factor), a pass over all N tiles at a time, so that a tile's sum is
-// not waited for by its next term.
+// D = A B, the same with nothing to add to
+__device__ __forceinline__ void lin_mma0(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(0.0f));
+}
+// Their products: lo hi + hi lo + hi hi (22 bits of each factor), a pass over all N tiles at a time, so that a tile's sum is
+// not waited for by its next term.  The tensor cores truncate what they add: eight terms are summed there, the small ones
+// first, and the eights in float32 (float32 outputs of 1500 rows, width 64, are 2.0e-7 off in the mean square so, and were
+// 1.1e-6 off with the accumulators left there; 2 to 5 % of the time).
 template <int N, bool SA, bool SB>
 __device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4, SA>& a, const LinFrag<2, SB> (&b)[N], int n) {
+  float u[N][4];
   if constexpr (SA) {
 #pragma unroll
     for (int y = 0; y < N; ++y)
-      if (y < n) lin_mma(d[y], a.lo, b[y].hi);
+      if (y < n) lin_mma0(u[y], a.lo, b[y].hi);
   }
   if constexpr (SB) {
 #pragma unroll
     for (int y = 0; y < N; ++y)
-      if (y < n) lin_mma(d[y], a.hi, b[y].lo);
+      if (y < n) {
+        if constexpr (SA) lin_mma(u[y], a.hi, b[y].lo);
+        else lin_mma0(u[y], a.hi, b[y].lo);
+      }
   }
 #pragma unroll
   for (int y = 0; y < N; ++y)
-    if (y < n) lin_mma(d[y], a.hi, b[y].hi);
+    if (y < n) {
+      if constexpr (SA || SB) lin_mma(u[y], a.hi, b[y].hi);
+      else lin_mma0(u[y], a.hi, b[y].hi);
+    }
+#pragma unroll
+  for (int y = 0; y < N; ++y)
+    if (y < n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[y][e] += u[y][e];
 }
 
 // One CTA: one (sequence, head, part, 64 columns of c), its chunks in turn; the
@@ -178,7 +199,7 @@ __device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4,
 // S is summed in float32 registers (the tensor cores truncate) and copied to
 // shared memory for the outputs.  What it is for is float32, which the tcgen05 kernel
 // does not take: 4 x 16 heads x 4096 rows of width 64 took 616 us by FP32 FMA with
-// 4 x 4 values a thread, which shared memory bounds, and take 320 us so.
+// 4 x 4 values a thread, which shared memory bounds, and take 338 us so.
 // STATE_ONLY leaves out the outputs: what the part adds to the state, from zero.
 template <typename T, int C, int DA, bool STATE_ONLY>
 __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_kernel(const __grid_constant__ LinPass P,

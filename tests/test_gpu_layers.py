@@ -513,6 +513,26 @@ def test_linear_long(dtype):
     check("ds0", grads[3][0], want[3], c * A[3])
 
 
+@pytest.mark.parametrize("dk, dv", [(64, 96), (128, 64), (40, 24)])
+def test_linear_mean_square(dk, dv):
+    """How far float32 results are off in the mean square, relative to theirs.  The sums are of terms of either sign, so what
+    is lost adds up by squares: over K terms, eights of them truncated at 2^-23 three times (3 2^-23 sqrt(8) sqrt(K / 8)
+    against sqrt(K), at 0.6 of the full truncation) give 2^-22.2, K / 8 <= 16 float32 sums 2^-24 sqrt(16 / 2) / sqrt(3) <=
+    2^-23.3, left-out products of two low halves 2^-24, the decay's powers at weights that count 2^-23: 2^-21.4 by squares,
+    where an accumulator that is truncated 48 times for one sign's worth of its value is off by 2^-20 and more."""
+    T, H = 1500, 4
+    g = torch.tensor([0.0, -0.004, -0.05, -0.7])
+    q, k, v, do = rnd(1, T, H, dk), rnd(2, T, 2, dk), rnd(3, T, 2, dv), rnd(4, T, H, dv)
+    att = pn.LinearAttention(H, 2, dk, dv, g, dtype=torch.float32)
+    dev = [x[None].cuda() for x in (q, k, v)]
+    o, S = att.forward(*dev)
+    got = (o[0], S[0], *[x[0] for x in att.backward(do[None].cuda(), *dev)[:3]])
+    want = (*lo.linear(q, k, v, g, dk ** -0.5), *lo.linear_gradient(do, q, k, v, g, dk ** -0.5)[:3])
+    for name, x, w in zip(("o", "S", "dq", "dk", "dv"), got, want):
+        off = ((x.double().cpu() - w).norm() / w.norm()).item()
+        assert off < 2.0 ** -21, f"{name}: {off:.3g}"
+
+
 def test_offsets_beyond_32_bits():
     """Rows whose element offsets, and states whose slots, pass 2^31."""
     far = 1 << 30
