@@ -70,14 +70,14 @@ size_t seg_bytes(const pn_linattn_s* h, int n_seq, long long max_len) {
 
 template <typename T, int C, int DA>
 cudaError_t launch_mma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
-  using K = LinMmaCfg<C, DA>;
+  using K = LinMmaCfg<T, C, DA>;
   const dim3 grid((P.dc + kLinDC - 1) / kLinDC, P.nseg, P.n_seq * P.H);
   cudaError_t e;
   if (P.nseg > 1) {
     if ((e = cudaFuncSetAttribute(lin_mma_kernel<T, C, DA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   K::SMEM_BYTES)) != cudaSuccess)
       return e;
-    lin_mma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), kLinThreads, K::SMEM_BYTES, st>>>(P, G);
+    lin_mma_kernel<T, C, DA, true><<<dim3(grid.x, P.nseg - 1, grid.z), K::NT, K::SMEM_BYTES, st>>>(P, G);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     lin_combine_kernel<<<dim3((P.da * P.dc + 511) / 512, P.n_seq * P.H), 128, 0, st>>>(P, G, C, 0);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -85,7 +85,7 @@ cudaError_t launch_mma(const LinPass& P, const LinDecay& G, cudaStream_t st) {
   if ((e = cudaFuncSetAttribute(lin_mma_kernel<T, C, DA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 K::SMEM_BYTES)) != cudaSuccess)
     return e;
-  lin_mma_kernel<T, C, DA, false><<<grid, kLinThreads, K::SMEM_BYTES, st>>>(P, G);
+  lin_mma_kernel<T, C, DA, false><<<grid, K::NT, K::SMEM_BYTES, st>>>(P, G);
   return cudaGetLastError();
 }
 

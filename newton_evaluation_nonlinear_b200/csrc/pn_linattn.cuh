@@ -102,10 +102,9 @@ template <typename T> __device__ __forceinline__ void lin_store4(T* p, int vec, 
   }
 }
 
-constexpr int kLinThreads = 256;
 constexpr int kLinDC = 64;     // columns of c one CTA takes
 
-template <int C, int DA>
+template <typename T, int C, int DA>
 struct LinMmaCfg {
   // Row strides in floats.  Fragments read rows (lane >> 2) and columns (lane & 3) of an A operand, and the other way round
   // of a B operand: strides of 12 and 8 banks keep both free of conflicts.
@@ -122,11 +121,14 @@ struct LinMmaCfg {
   static constexpr int SMEM_BYTES = (OFF_L + C + 4) * 4;
   static constexpr int CTAS = SMEM_BYTES <= 112 * 1024 ? 2 : 1;   // on an SM
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  // Sixteen warps where one CTA has the SM and operands need no splitting (4 x 16 heads x 4096 float16 rows of width 128
+  // 844 -> 742 us; float32, with more to do for each fragment that a warp reads, would lose, 906 -> 944).
   // warps: RT x CG over P's and the outputs' rows (16 each) and columns; MW x SG over S's
-  static constexpr int RT = C / 16, CG = 8 / RT;
-  static constexpr int NP = C / 8 / CG, NO = kLinDC / 8 / CG;
-  static_assert(C * DA / 4 % (4 * 256) == 0, "whole groups of loads");
-  static constexpr int MT = DA / 16, MW = MT < 8 ? MT : 8, SG = 8 / MW, MS = MT / MW, NS = kLinDC / 8 / SG;
+  static constexpr int NT = CTAS == 1 && sizeof(T) == 2 ? 512 : 256, NW = NT / 32;
+  static constexpr int RT = C / 16, CG = NW / RT;
+  static constexpr int NP = C / 8 > CG ? C / 8 / CG : 1, NO = kLinDC / 8 / CG;
+  static_assert(C * DA / 4 % (4 * NT) == 0, "whole groups of loads");
+  static constexpr int MT = DA / 16, MW = MT < 8 ? MT : 8, SG = NW / MW, MS = MT / MW, NS = kLinDC / 8 / SG;
 };
 
 // D += A B, 16 x 8 x 8 in TF32.  Lane (g, t) = (lane >> 2, lane & 3) holds rows g, g + 8 and columns t, t + 4 of A, rows
@@ -202,9 +204,9 @@ __device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4,
 // 4 x 4 values a thread, which shared memory bounds, and take 338 us so.
 // STATE_ONLY leaves out the outputs: what the part adds to the state, from zero.
 template <typename T, int C, int DA, bool STATE_ONLY>
-__global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_kernel(const __grid_constant__ LinPass P,
+__global__ void __launch_bounds__(LinMmaCfg<T, C, DA>::NT, LinMmaCfg<T, C, DA>::CTAS) lin_mma_kernel(const __grid_constant__ LinPass P,
                                                                                      const __grid_constant__ LinDecay G) {
-  using K = LinMmaCfg<C, DA>;
+  using K = LinMmaCfg<T, C, DA>;
   constexpr bool X = sizeof(T) == 4;   // inputs are split
   extern __shared__ __align__(16) float smem_lin[];
   float* sA = smem_lin + K::OFF_A;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
       }
   };
   if (!STATE_ONLY) publish();
-  for (int n = tid; n <= C; n += kLinThreads) sL[n] = lin_pow(l2, n);
+  for (int n = tid; n <= C; n += K::NT) sL[n] = lin_pow(l2, n);
   __syncthreads();
 
   const int wr = warp % K::RT, wc = warp / K::RT;
@@ -280,21 +282,21 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
     const int n = hi - r0 < C ? hi - r0 : C;   // rows of this chunk
     auto row_of = [&](int i) { return start + (P.reverse ? len - 1 - (r0 + i) : r0 + i); };
     // several loads in flight before their values are needed: a thread's 4 x 4 values of a and b at a time, then c's
-    constexpr int kC = C * kLinDC / 4 / kLinThreads;
+    constexpr int kC = C * kLinDC / 4 / K::NT;
     float cv[kC][4];
 #pragma unroll
     for (int x = 0; x < kC; ++x) {
-      const int e = tid + x * kLinThreads, i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
+      const int e = tid + x * K::NT, i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
 #pragma unroll
       for (int y = 0; y < 4; ++y) cv[x][y] = 0.0f;
       if (i < n && dc0 + j < dc) lin_load4<T>(cp + row_of(i) * P.c.ts + dc0 + j, P.vec, cv[x]);
     }
 #pragma unroll 1
-    for (int first = tid; first < C * DA / 4; first += 4 * kLinThreads) {
+    for (int first = tid; first < C * DA / 4; first += 4 * K::NT) {
       float av[4][4], bv[4][4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int e = first + x * kLinThreads, i = e / (DA / 4), d = 4 * (e % (DA / 4));
+        const int e = first + x * K::NT, i = e / (DA / 4), d = 4 * (e % (DA / 4));
 #pragma unroll
         for (int y = 0; y < 4; ++y) av[x][y] = bv[x][y] = 0.0f;
         if (i < n && d < da) {
@@ -305,14 +307,14 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int e = first + x * kLinThreads, i = e / (DA / 4), d = 4 * (e % (DA / 4));
+        const int e = first + x * K::NT, i = e / (DA / 4), d = 4 * (e % (DA / 4));
         if (!STATE_ONLY) *reinterpret_cast<float4*>(sA + i * K::PA + d) = make_float4(av[x][0], av[x][1], av[x][2], av[x][3]);
         *reinterpret_cast<float4*>(sB + i * K::PA + d) = make_float4(bv[x][0], bv[x][1], bv[x][2], bv[x][3]);
       }
     }
 #pragma unroll
     for (int x = 0; x < kC; ++x) {
-      const int e = tid + x * kLinThreads, i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
+      const int e = tid + x * K::NT, i = e / (kLinDC / 4), j = 4 * (e % (kLinDC / 4));
       const float (&v)[4] = cv[x];
       if (!STATE_ONLY) *reinterpret_cast<float4*>(sC + i * K::PV + j) = make_float4(v[0], v[1], v[2], v[3]);
       const float f = i < n ? P.alpha * sL[n - 1 - i] : 0.0f;
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kLinThreads, LinMmaCfg<C, DA>::CTAS) lin_mma_k
     if (r0 + C < hi) {
       const int m = min(C, hi - r0 - C);
       constexpr int kA = (DA * (int)sizeof(T) + 127) / 128, kV = kLinDC * (int)sizeof(T) / 128;
-      for (int e = tid; e < m * (2 * kA + kV); e += kLinThreads) {
+      for (int e = tid; e < m * (2 * kA + kV); e += K::NT) {
         const int i = C + e % m, l = e / m;   // row from r0 on, line: a's, b's, c's
         const int at = 128 / (int)sizeof(T) * (l < kA ? l : l < 2 * kA ? l - kA : l - 2 * kA);
         const long long r = row_of(i);
