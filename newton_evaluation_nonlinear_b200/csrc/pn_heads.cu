@@ -18,6 +18,11 @@
 // too few of them next to sines, weights and sums: each thread copies its pieces of
 // the next vectors to slots of its own in shared memory (cp.async), several vectors
 // ahead, over the borders of tokens too, and needs no barrier to read them.
+// Measured, bfloat16 of width 128: rotation of half of the head, 65536 rows x 20 heads,
+// interleaved, 115 us, 5.8 TB/s, 0.89 of the measured copy rate (183 us with the pieces loaded to
+// registers); norm and rotation of 16384 x 40 heads 73 us, 4.6 TB/s, 0.70 (143 us); its gradient
+// 129 us, 3.9 TB/s, 0.59 (272 us): what is left there is the sums over a group's lanes, the
+// sines and the two products for each value, all in float32.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>

@@ -196,7 +196,7 @@ __device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4,
 }
 
 // One CTA: one (sequence, head, part, 64 columns of c), its chunks in turn; the
-// four products of a chunk by eight warps on the TF32 tensor cores (mma.sync), in
+// four products of a chunk by all warps on the TF32 tensor cores (mma.sync), in
 // split form: 16-bit operands are TF32 values as they are, everything else takes two.
 // S is summed in float32 registers (the tensor cores truncate) and copied to
 // shared memory for the outputs.  What it is for is float32, which the tcgen05 kernel
@@ -594,7 +594,8 @@ constexpr int kStepThreads = 256;
 // the state's one read and one write.  A CTA takes CX * 4 columns of one state;
 // a thread four columns of every RG-th row, so that a warp reads whole lines.
 // Norm and rotation of q and k, where asked for, are done by two warps while
-// the state's first rows are on their way.
+// the state's first rows are on their way.  192 rows x 32 heads of 128 x 128: 133 us, 6.1 TB/s,
+// 0.92 of the measured copy rate.
 template <typename T, int CX>
 __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_constant__ LinStep P,
                                                                 const __grid_constant__ LinDecay G) {

@@ -1,10 +1,11 @@
 // pn_linattn_tc.cuh -- linear attention over whole sequences on the tensor cores
-// (tcgen05), for 16-bit operands of widths up to 128.
+// (tcgen05), for bfloat16 operands of widths a, b up to 128 (float16 would need a scale for every row of P and of S:
+// neither stays within its range; wider ones do not fit TMEM and shared memory beside three chunks in flight).
 //
 // One pass of pn_linattn.cuh by chunks of C = 64 rows.  One CTA owns one
 // (sequence, head, part) and takes its chunks in turn; the state S^T (dc x da,
-// float32) never leaves the SM: it sits in TMEM.  Per chunk, all from operands that
-// TMA brought in 128-byte swizzled rows:
+// float32) never leaves the SM: it sits in the registers of eight warps.  Per chunk, all from operands
+// that TMA brought in 128-byte swizzled rows:
 //   P    = a b^T                          64 x 64     (masked, weighted, rounded: P~)
 //   O1^T = S~^T a^T                       dc x 64     (S~: S rounded to the operands' type)
 //   O2^T = c^T P~^T                       dc x 64
@@ -37,11 +38,16 @@
 // The chain from chunk to chunk is U and its sum; S~ and O1 hang off it.  At dc = 128 the pieces
 // of c' lie in TMEM, transposed on their way by ldmatrix: an operand less for shared memory to
 // feed (two such operands of a 128 x 128 x 16 step are its whole bandwidth), and room for a third
-// chunk in flight.  At dc = 64 they lie in shared memory.  What bounds the rest is instructions (all roles share four schedulers): accumulators are read in the
-// 16 x 256-bit fragments, in which every lane holds values whatever M is and two neighbours
-// sit in one thread, and go to shared memory by stmatrix, transposed for the outputs.  Loops
-// of several hundred instructions are rolled (unrolled, five roles overran the instruction
-// cache: 3.7 stalls for each instruction issued).
+// chunk in flight.  At dc = 64 they lie in shared memory.
+//
+// What bounds the rest is instructions and the waits between the roles, which share four schedulers:
+// accumulators are read in the 16 x 256-bit fragments, in which every lane holds values whatever M is and
+// two neighbours sit in one thread, and go to shared memory by stmatrix, transposed for the outputs.
+// Loops of several hundred instructions are rolled (unrolled, five roles overran the instruction
+// cache: 3.7 stalls for each instruction issued; 2.1 rolled).
+// Measured, 4 x 37 heads x 4096 rows (one CTA on every SM): width 128 127 us, 4.9 TB/s of the arrays'
+// bytes, 0.74 of the measured copy rate, 0.58 instructions a scheduler and clock, tensor cores
+// busy half of the time; width 64 76 us, 4.1 TB/s.
 #pragma once
 
 #include <type_traits>
