@@ -232,7 +232,8 @@ pn_status pn_linattn_create(pn_linattn* out, int H, int Hkv, int dk, int dv, int
   h->dv = dv;
   h->dtype = dtype;
   h->scale = scale;
-  for (int i = 0; i < H; ++i) h->log2_decay[i] = (float)((double)log_decay[i] * 1.4426950408889634074);
+  // (2^-1e30 is zero as well, and its multiples by zero are zero: an infinite exponent's are not)
+  for (int i = 0; i < H; ++i) h->log2_decay[i] = (float)std::max((double)log_decay[i] * 1.4426950408889634074, -1e30);
   *out = h;
   return PN_OK;
 }

@@ -513,6 +513,35 @@ def test_linear_long(dtype):
     check("ds0", grads[3][0], want[3], c * A[3])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_linear_strongest_decays(dtype):
+    """Decays down to the least float32: nothing is kept, and no exponent becomes a NaN (bounds as in run_linear: every sum
+    has one term)."""
+    n, T, H, d = 2, 70, 4, 64
+    g = torch.tensor([-3.4e38, -1e38, -1e6, -0.5])
+    q, k, v, do = (rnd(i, n, T, H, d, dtype=dtype) for i in range(4))
+    s0, ds = rnd(5, n, H, d, d), rnd(6, n, H, d, d)
+    att = pn.LinearAttention(H, H, d, d, g, dtype=dtype)
+    dev = [x.cuda() for x in (q, k, v)]
+    o, S = att.forward(*dev, initial_state=s0.cuda())
+    grads = att.backward(do.cuda(), *dev, initial_state=s0.cuda(), dstate=ds.cuda())
+    states = s0.cuda()
+    o1 = att.step(*[x[:, 0] for x in dev], states)
+    u, m, c = half_step(dtype), mixed(dtype), 2.0 ** -17
+    for i in range(n):
+        a, mag = (q[i], k[i], v[i]), [x[i].double().abs() for x in (q, k, v)]
+        wo, wS = lo.linear(*a, g, d ** -0.5, s0[i])
+        Ao, AS = lo.linear(*mag, g, d ** -0.5, s0[i].abs())
+        check("o", o[i], wo, u * wo.abs() + (m + c) * Ao)
+        check("S", S[i], wS, c * AS)
+        want = lo.linear_gradient(do[i], *a, g, d ** -0.5, s0[i], ds[i])
+        A = lo.linear_gradient(do[i].double().abs(), *mag, g, d ** -0.5, s0[i].abs(), ds[i].abs())
+        for name, x, w, y in zip(("dq", "dk", "dv"), grads, want, A):
+            check(name, x[i], w, u * w.abs() + (m + c) * y)
+        check("ds0", grads[3][i], want[3], c * A[3])
+        check("step", o1[i], wo[0], u * wo[0].abs() + (m + c) * Ao[0])
+
+
 @pytest.mark.parametrize("dk, dv", [(64, 96), (128, 64), (40, 24)])
 def test_linear_mean_square(dk, dv):
     """How far float32 results are off in the mean square, relative to theirs.  The sums are of terms of either sign, so what
