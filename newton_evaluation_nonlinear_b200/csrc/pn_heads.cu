@@ -19,9 +19,9 @@
 // the next vectors to slots of its own in shared memory (cp.async), several vectors
 // ahead, over the borders of tokens too, and needs no barrier to read them.
 // Measured, bfloat16 of width 128: rotation of half of the head, 65536 rows x 20 heads,
-// interleaved, 115 us, 5.8 TB/s, 0.89 of the measured copy rate (183 us with the pieces loaded to
-// registers); norm and rotation of 16384 x 40 heads 73 us, 4.6 TB/s, 0.70 (143 us); its gradient
-// 129 us, 3.9 TB/s, 0.59 (272 us): what is left there is the sums over a group's lanes, the
+// interleaved, 110 us, 6.1 TB/s, 0.93 of the measured copy rate (183 us with the pieces loaded to
+// registers); norm and rotation of 16384 x 40 heads 65 us, 5.1 TB/s, 0.78 (143 us); its gradient
+// 116 us, 4.3 TB/s, 0.66 (272 us): what is left there is the sums over a group's lanes, the
 // sines and the two products for each value, all in float32.
 #include <algorithm>
 #include <cmath>
@@ -66,7 +66,7 @@ struct HeadsArgs {
   long long rows;        // B * T
   int heads[2];          // query and key heads
   int blocks[2];         // blocks of hb heads per token
-  int hb;
+  int hb[2];
   int dim, rot;
   int half_units;        // units that hold rotated pairs of the half layout (0: interleaved)
   int units;
@@ -122,8 +122,8 @@ struct HeadsItem {
       kind = 1;
       blk -= A.blocks[0];
     }
-    h0 = blk * A.hb;
-    h1 = min(A.heads[kind], h0 + A.hb);
+    h0 = blk * A.hb[kind];
+    h1 = min(A.heads[kind], h0 + A.hb[kind]);
   }
 };
 
@@ -446,7 +446,7 @@ bool aligned_to(const pn_heads* h, size_t es, int ve) {
          h->head_stride % ve == 0;
 }
 
-constexpr int kGradCtasPerSm = 4;
+constexpr int kGradCtasPerSm = 2;   // as many as run at once: each starts and sums once (4: 131 us in place of 116 at 16384 x 40 heads of 128)
 
 // CTAs of the gradient: queries first, then keys, in the ratio of their heads
 void grad_grid(long long rows, int Hq, int Hk, int* gq, int* gk) {
@@ -591,9 +591,10 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
   const long long vectors = rows * (Hq + Hk);
   int hb = 1;
   while (hb < 8 && vectors / (2 * hb) >= 148LL * 4 * per_cta) hb <<= 1;
-  A.hb = hb;
-  A.blocks[0] = (Hq + hb - 1) / hb;
-  A.blocks[1] = (Hk + hb - 1) / hb;
+  for (int i = 0; i < 2; ++i) {   // in blocks of nearly one size (12 heads: 6 and 6, not 8 and 4)
+    A.blocks[i] = (A.heads[i] + hb - 1) / hb;
+    A.hb[i] = (A.heads[i] + A.blocks[i] - 1) / A.blocks[i];
+  }
 
   int grid;
   size_t smem = 0;
@@ -608,7 +609,12 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
     A.partial = (float*)ws;
   } else {
     const long long items = rows * (A.blocks[0] + A.blocks[1]);
-    grid = (int)std::min<long long>((items + per_cta - 1) / per_cta, 148LL * 16);
+    // Where instructions bound it (the norm of 16-bit vectors; groups with idle lanes), as many CTAs as run at once, each with a
+    // long list, else more and shorter ones, which even out the SMs' shares of the memory: 3 against 16 on an SM, norm of 16384 x
+    // 40 bfloat16 heads of 128 65 and 73 us, rotation of 6135 x 24 float32 heads of 80 21 and 23; rotation of 65536 x 20 bfloat16
+    // heads of 128 128 and 109, norm of 16384 x 20 float32 heads of 128 67 and 61.
+    const bool busy = ve > 1 && ((norm && es == 2) || A.units < group);
+    grid = (int)std::min<long long>((items + per_cta - 1) / per_cta, 148LL * (busy ? 3 : 16));
   }
   // the slots; the gradient's sums lie in the same memory
   smem = ve == 1 ? 0 : (size_t)ahead(grad) * (grad ? 4 : 2) * kHeadThreads * ve * es;
