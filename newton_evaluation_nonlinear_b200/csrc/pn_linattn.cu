@@ -34,12 +34,13 @@ LinOperand operand(const pn_heads* x, int per) {
 // Rows of one chunk of the kernels for any type and width.
 int mma_chunk(int da) { return da <= 128 ? 64 : 32; }
 
-// Parts a sequence is cut into there: as many as fit the card beside each other (two CTAs on an SM up to width 64), of four
-// chunks at least (a part costs a second read of two operands and half the work).
+// Parts a sequence is cut into there: as many as fit the card beside each other (two CTAs on an SM up to width 64).  A part's
+// state alone takes a third of its outputs' time, so parts of one chunk pay where SMs are idle (float32, 8 heads of width 64,
+// 512 rows: 20 us, 54 in parts of four); where a second CTA on an SM is all there is to win, which is little, parts have four chunks.
 int mma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int dc) {
-  const long long ctas = (long long)n_seq * h->H * ((dc + kLinDC - 1) / kLinDC);
-  const long long want = 148 * (da <= 64 ? 2 : 1) / std::max(1LL, ctas);
-  return (int)std::max(1LL, std::min(want, max_len / (4 * mma_chunk(da))));
+  const long long ctas = std::max(1LL, (long long)n_seq * h->H * ((dc + kLinDC - 1) / kLinDC));
+  const long long want = 148 * (da <= 64 ? 2 : 1) / ctas;
+  return (int)std::max(1LL, std::min(want, max_len / (mma_chunk(da) * (2 * ctas <= 148 ? 1 : 4))));
 }
 
 // Columns of c that one CTA of the tensor-core kernel takes: 64 where 128 leave SMs idle (a and b are then read twice, out of
@@ -48,12 +49,15 @@ int tc_columns(const pn_linattn_s* h, int n_seq, int dc) {
   return dc <= 64 || (long long)n_seq * h->H * ((dc + 63) / 64) <= 148 ? 64 : 128;
 }
 
-// Parts for the tensor-core kernel: a CTA fills its SM, so as many as fit the card beside each other.
+// Parts for the tensor-core kernel: a CTA fills its SM, so as many as fit the card beside each other, of four chunks at least.
+// A part's state alone takes three quarters of its outputs' time, and the two launches more take that of 10 chunks or so, so p
+// parts of n chunks pay from n (1 - 1.75 / p) = 10 on (32 heads of width 128, 1024 rows: 25 us whole, 34 in two parts; 2 heads
+// of width 64, 2048 rows: 19 us in eight parts, 24 in four).
 int tc_parts(const pn_linattn_s* h, int n_seq, long long max_len, int dc) {
   const int w = tc_columns(h, n_seq, dc);
-  const long long ctas = (long long)n_seq * h->H * ((dc + w - 1) / w);
-  const long long want = 148 / std::max(1LL, ctas);
-  return (int)std::max(1LL, std::min(want, max_len / (4 * 64)));
+  const long long ctas = std::max(1LL, (long long)n_seq * h->H * ((dc + w - 1) / w));
+  const long long n = (max_len + 63) / 64, p = std::min(148 / ctas, max_len / (4 * 64));
+  return p > 1 && 4 * n * p - 7 * n >= 40 * p ? (int)p : 1;
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
