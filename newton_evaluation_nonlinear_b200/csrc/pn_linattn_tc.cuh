@@ -716,9 +716,9 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     };
     // Against time the first chunk's rows (a short chunk, or the last row undecayed) see the state this much earlier than
     // those of a whole one, for which the row factors and P~ are made: it enters that much larger, and decays as over a
-    // whole chunk.
+    // whole chunk.  (No rows, no frame: the state of an empty sequence passes as it is.)
     const int early = P.reverse && !two && M > 0 && !STATE_ONLY ? C - rows_of(0) + e0 : 0;
-    const float lead = frame * exp2f(-l2 * (float)early);
+    const float lead = M > 0 ? frame * exp2f(-l2 * (float)early) : 1.0f;
     float S[NB][NQ][16] = {};
     if (src) {
       float* x = stage_of(1 + hi_half);
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar_init);
-    if (!two) f_out *= exp2f(-l2 * R);
+    if (!two && M > 0) f_out *= exp2f(-l2 * R);
     if (STATE_ONLY) f_out = 1.0f;
     const float f_full = lin_pow(l2, C);
     bool ok = true;

@@ -1,0 +1,35 @@
+"""Calls of the sequence-layer operators at the edges of what their documentation allows: empty sequences, elements that do
+not rotate, offsets out of order, outputs of unusual inputs, and the kernels that only larger grids reach.
+
+Bounds are those of test_gpu_layers.py, which derives them; what is compared bit for bit here has no rounding in it.
+"""
+import pytest
+import torch
+
+import newton_evaluation_nonlinear_b200 as pn
+from test_gpu_layers import TYPES, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n_copies, dk, dv", [(1, 64, 64), (1, 128, 96), (20, 128, 128)])
+def test_empty_sequences_keep_their_states(n_copies, dk, dv, dtype):
+    """The final state of an empty sequence is its initial one, and the gradient of its initial state that of its final one,
+    to the last bit, whatever the decays and the size of the values."""
+    lens = [0, 5, 0, 130, 64, 1, 0] * n_copies
+    n, H, K, T = len(lens), 4, 2, sum(lens)
+    att = pn.LinearAttention(H, K, dk, dv, [-1e-3, -0.05, -0.8, -3.0], dtype=dtype)
+    q, do = rnd(1, T, H, dk, dtype=dtype).cuda(), rnd(2, T, H, dv, dtype=dtype).cuda()
+    k, v = rnd(3, T, K, dk, dtype=dtype).cuda(), rnd(4, T, K, dv, dtype=dtype).cuda()
+    s0, ds = rnd(5, n, H, dk, dv).cuda(), rnd(6, n, H, dk, dv).cuda()
+    s0[:, :, 1] *= 1e-35   # small enough that a detour by way of other powers of two would lose bits
+    ds[:, :, 2] *= 1e30
+    cu = torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    o, S = att.forward(q, k, v, initial_state=s0, cu_seqlens=cu, max_len=130)
+    ds0 = att.backward(do, q, k, v, initial_state=s0, dstate=ds, cu_seqlens=cu, max_len=130)[3]
+    for i, length in enumerate(lens):
+        if length == 0:
+            assert torch.equal(S[i], s0[i]) and torch.equal(ds0[i], ds[i]), i
+    o, S = att.forward(q[:0], k[:0], v[:0], initial_state=s0, cu_seqlens=torch.zeros_like(cu))   # nothing but empty ones
+    assert torch.equal(S, s0)
