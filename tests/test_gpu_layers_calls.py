@@ -33,3 +33,29 @@ def test_empty_sequences_keep_their_states(n_copies, dk, dv, dtype):
             assert torch.equal(S[i], s0[i]) and torch.equal(ds0[i], ds[i]), i
     o, S = att.forward(q[:0], k[:0], v[:0], initial_state=s0, cu_seqlens=torch.zeros_like(cu))   # nothing but empty ones
     assert torch.equal(S, s0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim, rot, layout", [(128, 64, "half"), (128, 64, "interleaved"), (72, 24, "half"), (40, 12, "half"),
+                                              (40, 12, "interleaved"), (10, 6, "half"), (10, 6, "interleaved"), (256, 8, "half"),
+                                              (256, 2, "interleaved")])
+def test_elements_that_do_not_rotate_pass_through(dim, rot, layout, dtype):
+    """Elements behind rot_dim come out as they went in, infinities, NaN and negative zeros too, and reach no other element."""
+    B, T, H, K = 2, 5, 3, 1
+    r = pn.Rotary(rot, layout=layout, scaling="yarn", factor=4.0)
+    pos = (torch.arange(T)[None] + torch.tensor([[0], [99]])).cuda()
+    clean = [rnd(i, B, T, h, dim, dtype=dtype).cuda() for i, h in ((1, H), (2, K))]
+    odd = torch.tensor([float("inf"), float("-inf"), float("nan"), -0.0, 1.0], dtype=dtype, device="cuda")
+    gen = torch.Generator().manual_seed(3)
+    filled = []
+    for x in clean:
+        x = x.clone()
+        x[..., rot:] = odd[torch.randint(0, 5, (*x.shape[:-1], dim - rot), generator=gen).cuda()]
+        filled.append(x)
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    for call in (r.apply, r.apply_backward):
+        for x, got, want in zip(filled, call(*filled, pos), call(*clean, pos)):
+            assert torch.equal(got[..., :rot], want[..., :rot])
+            a, b = got[..., rot:], x[..., rot:]
+            assert torch.equal(a.isnan(), b.isnan())
+            assert torch.equal(a.contiguous().view(bits)[~a.isnan()], b.contiguous().view(bits)[~b.isnan()])
