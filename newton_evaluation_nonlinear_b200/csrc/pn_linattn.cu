@@ -182,11 +182,12 @@ cudaError_t run_pass(const pn_linattn_s* h, LinPass P, int n_seq, long long max_
 template <typename T>
 cudaError_t group_sum(const float* part, long long rows, int H, int G, int d, const pn_heads* dst, long long tokens,
                       const int* cu, int n_seq, cudaStream_t st) {
-  const int grid = (int)std::min<long long>(rows, 148LL * 16);
+  // (sequences differ in length: more and shorter shares than CTAs that run at once)
+  const dim3 grid((unsigned)std::min<long long>(rows, cu ? (148LL * 64 + n_seq - 1) / n_seq : 148LL * 16), cu ? n_seq : 1);
   const bool vec = (uintptr_t)dst->data % (4 * sizeof(T)) == 0 && dst->batch_stride % 4 == 0 && dst->token_stride % 4 == 0 &&
                    dst->head_stride % 4 == 0;
   lin_group_sum_kernel<T><<<grid, 256, 0, st>>>(part, rows, H, G, d, (T*)dst->data, dst->batch_stride, dst->token_stride,
-                                               dst->head_stride, tokens, cu, n_seq, vec);
+                                               dst->head_stride, tokens, cu, vec);
   return cudaGetLastError();
 }
 

@@ -60,15 +60,19 @@ struct LinDecay {
   float log2[kMaxLinHeads];
 };
 
-// The rows of sequence s.  Offsets come from the device: whatever they say,
+// The rows lo .. hi - 1 of sequence s of a buffer of T rows.  Offsets come from the device: whatever they say,
 // rows stay inside the buffer.
+__device__ __forceinline__ void lin_span(const int* cu, long long T, int s, long long& lo, long long& hi) {
+  lo = cu[s];
+  hi = cu[s + 1];
+  lo = lo < 0 ? 0 : lo > T ? T : lo;
+  hi = hi < lo ? lo : hi > T ? T : hi;
+}
 __device__ __forceinline__ void lin_rows(const LinPass& P, int s, long long& start, int& len) {
   if (P.cu) {
-    long long lo = P.cu[s], hi = P.cu[s + 1];
-    lo = lo < 0 ? 0 : lo > P.T ? P.T : lo;
-    hi = hi < lo ? lo : hi > P.T ? P.T : hi;
-    start = lo;
-    len = (int)(hi - lo);
+    long long hi;
+    lin_span(P.cu, P.T, s, start, hi);
+    len = (int)(hi - start);
   } else {
     start = 0;
     len = (int)P.T;
@@ -538,17 +542,15 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
 
 // dst = sum of the partial gradients [rows][H][d] of each group of heads, in the
 // order of the heads, four neighbours to a thread; rows of no sequence are left as
-// they are.  A block takes whole rows of K heads.
+// they are: with offsets, a CTA takes rows of the sequence blockIdx.y, as the passes
+// that wrote them did.  A block takes whole rows of K heads.
 template <typename T>
 __global__ void __launch_bounds__(256) lin_group_sum_kernel(const float* __restrict__ part, long long rows, int H, int G,
                                                             int d, T* dst, long long bs, long long ts, long long hs,
-                                                            long long tokens, const int* cu, int n_seq, int vec) {
+                                                            long long tokens, const int* cu, int vec) {
   const int K = H / G, quads = K * d / 4;
   long long lo = 0, hi = rows;
-  if (cu) {
-    lo = max(0LL, (long long)cu[0]);
-    hi = min(rows, (long long)cu[n_seq]);
-  }
+  if (cu) lin_span(cu, rows, blockIdx.y, lo, hi);
   for (long long r = lo + blockIdx.x; r < hi; r += gridDim.x) {
     const long long b = r / tokens, t = r - b * tokens;
     T* out = dst + b * bs + t * ts;

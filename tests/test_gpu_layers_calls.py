@@ -59,3 +59,51 @@ def test_elements_that_do_not_rotate_pass_through(dim, rot, layout, dtype):
             a, b = got[..., rot:], x[..., rot:]
             assert torch.equal(a.isnan(), b.isnan())
             assert torch.equal(a.contiguous().view(bits)[~a.isnan()], b.contiguous().view(bits)[~b.isnan()])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [1, 2])
+def test_gradients_with_offsets_out_of_order(K, dtype):
+    """Gradients take the rows that the forward pass takes whatever the offsets say, shared heads included: offsets outside the
+    buffer are cut to it and a decreasing one makes an empty sequence."""
+    T, H, d = 200, 2, 64
+    att = pn.LinearAttention(H, K, d, d, [-0.05, -0.8], dtype=dtype)
+    q, do = rnd(1, T, H, d, dtype=dtype).cuda(), rnd(2, T, H, d, dtype=dtype).cuda()
+    k, v = rnd(3, T, K, d, dtype=dtype).cuda(), rnd(4, T, K, d, dtype=dtype).cuda()
+    s0, ds = rnd(5, 3, H, d, d).cuda(), rnd(6, 3, H, d, d).cuda()
+
+    def run(cu):
+        grads = tuple(torch.full_like(x, 7.0) for x in (q, k, v))
+        return att.backward(do, q, k, v, initial_state=s0, dstate=ds, max_len=T, grads=grads,
+                            cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+
+    for bad, good in (([-5, 90, 90, 1000000], [0, 90, 90, T]), ([0, 120, 60, 60], [0, 120, 120, 120]),
+                      ([150, 2 ** 31 - 1, 40, 40], [150, T, T, T]), ([190, 100, 100, 160], [100, 100, 100, 160])):
+        for name, a, b in zip(("dq", "dk", "dv", "ds0"), run(bad), run(good)):
+            assert torch.equal(a, b), (bad, name)
+    dq, dk, dv, _ = run([190, 100, 100, 160])   # rows of no sequence are left as they were
+    for x in (dq, dk, dv):
+        assert bool((x[:100] == 7).all()) and bool((x[160:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients_of_shared_heads_in_many_sequences(dtype):
+    """Sequences of very different lengths beside each other: each row of dk and dv is that of its sequence alone, to the bit
+    where both runs take the same parts."""
+    H, K, d = 4, 1, 16
+    lens = [(5 * i) % 7 for i in range(300)] + [400, 0, 131]
+    T = sum(lens) + 9
+    cu = torch.tensor([sum(lens[:i]) for i in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+    att = pn.LinearAttention(H, K, d, d, [-0.01, -0.1, -0.9, -3.0], dtype=dtype)
+    q, do = rnd(1, T, H, d, dtype=dtype).cuda(), rnd(2, T, H, d, dtype=dtype).cuda()
+    k, v = rnd(3, T, K, d, dtype=dtype).cuda(), rnd(4, T, K, d, dtype=dtype).cuda()
+    grads = tuple(torch.full_like(x, 7.0) for x in (q, k, v))
+    att.backward(do, q, k, v, cu_seqlens=cu, max_len=400, grads=grads)
+    for i in (0, 1, 3, 299, 300, 302):
+        r = slice(int(cu[i]), int(cu[i + 1]))
+        one = torch.tensor([0, lens[i]] + [lens[i]] * (len(lens) - 1), dtype=torch.int32, device="cuda")
+        alone = att.backward(do[r], q[r], k[r], v[r], cu_seqlens=one, max_len=400)
+        for x, y in zip(grads, alone):
+            assert torch.equal(x[r], y), i
+    for x in grads:
+        assert bool((x[T - 9:] == 7).all())
