@@ -37,6 +37,7 @@ struct LinPass {
   long long out_bs, out_ts, out_hs;
   int out_f32;             // out is float32 (partial gradients of shared heads)
   int out_map;             // whole chunks of out are stored by TMA
+  int by_length;           // sequences are taken longest first
   int vec;                 // every row of the four arrays is aligned to four elements
   int da, dc;              // widths: a and b, c and out
   int H, n_seq;

@@ -288,7 +288,49 @@ struct LinMaps {
   CUtensorMap a, b, c, o;
 };
 
-constexpr int kLinSorted = 512;   // up to this many sequences are taken by length (each CTA ranks them: n^2 / 896 steps a thread)
+constexpr int kLinSorted = 512;   // up to this many sequences can be taken by length
+
+// The sequence with `s` others before it by length in chunks, equal ones in their order; n <= kLinSorted of them.  Every CTA asks:
+// one warp finds the s-th largest key, a bit at a time (each of n threads ranking one against all took a CTA 30 us at 512
+// sequences).  All threads call it.
+template <int NT>
+__device__ __forceinline__ int lin_by_length(const int* cu, long long T, int n, int s) {
+  __shared__ unsigned s_key[kLinSorted];
+  __shared__ int s_seq;
+  for (int i = threadIdx.x; i < kLinSorted; i += NT) {
+    unsigned key = 0;
+    if (i < n) {
+      long long lo, hi;
+      lin_span(cu, T, i, lo, hi);
+      const long long chunks = (hi - lo + 63) / 64;
+      key = (unsigned)(chunks < (1 << 22) - 1 ? chunks : (1 << 22) - 1) << 10 | (unsigned)(1023 - i);
+    }
+    s_key[i] = key;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    unsigned key[kLinSorted / 32], top = 0;
+#pragma unroll
+    for (int x = 0; x < kLinSorted / 32; ++x) {
+      key[x] = s_key[threadIdx.x + 32 * x];
+      top = max(top, key[x]);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    unsigned found = 0;   // the largest value that more than s keys reach
+#pragma unroll 1
+    for (unsigned bit = 1u << (31 - __clz(top)); bit; bit >>= 1) {
+      int reach = key[0] >= (found | bit);
+      if (n > 32) {
+#pragma unroll
+        for (int x = 1; x < kLinSorted / 32; ++x) reach += key[x] >= (found | bit);
+      }
+      if (__reduce_add_sync(0xffffffffu, reach) > s) found |= bit;
+    }
+    if (threadIdx.x == 0) s_seq = 1023 - (int)(found & 1023u);
+  }
+  __syncthreads();
+  return s_seq;
+}
 
 template <int DA, int DC>
 struct LinTcCfg {
@@ -340,24 +382,10 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // CTAs start in the order of their numbers, each for the whole of its part: the longest sequences first, so that no long
-  // one starts late (16 sequences of 0 .. 3800 rows, 32 heads of width 128: 394 -> 342 us)
+  // one starts late, where that can matter (the rule is the caller's)
   const int h = blockIdx.y % P.H;
   int s = blockIdx.y / P.H;
-  if (P.cu && P.n_seq > 1 && P.n_seq <= kLinSorted) {
-    __shared__ int s_seq;
-    for (int i = threadIdx.x; i < P.n_seq; i += K::NT) {
-      long long at;
-      int li, lj, rank = 0;
-      lin_rows(P, i, at, li);
-      for (int j = 0; j < P.n_seq; ++j) {
-        lin_rows(P, j, at, lj);
-        rank += lj > li || (lj == li && j < i);
-      }
-      if (rank == s) s_seq = i;
-    }
-    __syncthreads();
-    s = s_seq;
-  }
+  if (P.by_length) s = lin_by_length<K::NT>(P.cu, P.T, P.n_seq, s);
   const int sh = s * P.H + h;
   const int dc0 = blockIdx.x * DC;
   const int part = blockIdx.z;

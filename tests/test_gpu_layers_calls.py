@@ -107,3 +107,30 @@ def test_gradients_of_shared_heads_in_many_sequences(dtype):
             assert torch.equal(x[r], y), i
     for x in grads:
         assert bool((x[T - 9:] == 7).all())
+
+
+@pytest.mark.parametrize("n", [2, 33, 512, 513])
+def test_order_of_sequences_does_not_matter(n):
+    """Sequences are taken by length; packed in another order each gives the same bits."""
+    H, d = 2, 64
+    gen = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 150, (n,), generator=gen).tolist()
+    lens[n // 2] = 700
+    lens[n - 1] = lens[0]
+    T = sum(lens)
+    att = pn.LinearAttention(H, H, d, d, [-0.01, -0.9], dtype=torch.bfloat16)
+    x = [rnd(i, T, H, d, dtype=torch.bfloat16) for i in (1, 2, 3)]
+    s0 = rnd(4, n, H, d, d)
+    parts = [list(y.split(lens)) for y in x]
+
+    def run(order):
+        cu = torch.tensor([0] + [lens[i] for i in order]).cumsum(0).int().cuda()
+        packed = [torch.cat([p[i] for i in order]).cuda() for p in parts]
+        o, S = att.forward(*packed, initial_state=s0[order].cuda(), cu_seqlens=cu, max_len=700)
+        rows = dict(zip(order, o.split([lens[i] for i in order])))
+        return [rows[i] for i in range(n)], S[torch.tensor(order).argsort().cuda()]
+
+    o, S = run(list(range(n)))
+    o2, S2 = run(torch.randperm(n, generator=gen).tolist())
+    assert torch.equal(S, S2)
+    assert all(torch.equal(a, b) for a, b in zip(o, o2))
