@@ -107,6 +107,14 @@ def _output(name, t, like, heads, dim):
     return row
 
 
+def _like(t):
+    """A tensor like t, laid out as it is where that leaves rows contiguous.  (empty_like orders dimensions by their strides;
+    windows that overlap by all but one element have two of one element, and their rows need not come out last.)"""
+    import torch
+    o = torch.empty_like(t)
+    return o if o.stride(-1) == 1 else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _fresh(t, nd):
     """The same of a tensor just made."""
     if nd == 4:
@@ -215,10 +223,9 @@ class Rotary:
 
     @staticmethod
     def _out(q, k, like, K, out):
-        import torch
         nd, _, _, H, d, _, _ = like
         if out is None:
-            oq, ok = torch.empty_like(q), torch.empty_like(k)
+            oq, ok = _like(q), _like(k)
             return (oq, ok), _fresh(oq, nd), _fresh(ok, nd)
         oq, ok = out
         return (oq, ok), _output("out[0]", oq, like, H, d), _output("out[1]", ok, like, K, d)
@@ -331,8 +338,7 @@ class LinearAttention:
                 int(max_len or 0))
 
     def _empty(self, q):
-        import torch
-        return torch.empty_like(q) if self.dv == self.dk else q.new_empty(q.shape[:-1] + (self.dv,))
+        return _like(q) if self.dv == self.dk else q.new_empty(q.shape[:-1] + (self.dv,))
 
     def forward(self, q, k, v, initial_state=None, cu_seqlens=None, max_len: Optional[int] = None, out=None):
         """(o, final state) of whole sequences.
@@ -370,7 +376,7 @@ class LinearAttention:
         s0 = _float32("initial_state", initial_state, shape, device)
         ds = _float32("dstate", dstate, shape, device)
         if grads is None:
-            grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+            grads = (_like(q), _like(k), _like(v))
         sizes = ((self.heads, self.dk), (self.kv_heads, self.dk), (self.kv_heads, self.dv))
         outs = [_output(f"grads[{i}]", g, like, *size) for i, (g, size) in enumerate(zip(grads, sizes))]
         ds0 = q.new_empty(shape, dtype=torch.float32)

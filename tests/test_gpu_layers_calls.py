@@ -134,3 +134,32 @@ def test_order_of_sequences_does_not_matter(n):
     o2, S2 = run(torch.randperm(n, generator=gen).tolist())
     assert torch.equal(S, S2)
     assert all(torch.equal(a, b) for a, b in zip(o, o2))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_windows_that_overlap(dtype):
+    """Heads that are windows of one row, each an element on from the one before (any strides are allowed): results are those of
+    a copy, and come in tensors of their own with contiguous rows."""
+    T, H, d = 70, 4, 64
+    base = rnd(1, T, d + H - 1, dtype=dtype).cuda()
+    x = base.as_strided((T, H, d), (d + H - 1, 1, 1))
+    y = x.clone(memory_format=torch.contiguous_format)
+    pos, w = torch.arange(T, device="cuda"), rnd(2, d).cuda()
+    r, att = pn.Rotary(d), pn.LinearAttention(H, H, d, d, [0.0, -0.05, -0.8, -3.0], dtype=dtype)
+    s0 = rnd(3, 1, H, d, d).cuda()
+    one = dict(initial_state=s0, cu_seqlens=torch.tensor([0, T], dtype=torch.int32, device="cuda"))
+    for a, b in zip(r.apply(x, x, pos), r.apply(y, y, pos)):
+        assert torch.equal(a, b)
+    for a, b in zip((*r.norm_apply(x, x, pos, w, w), *r.norm_backward(x, x, x, x, pos, w, w)[:2]),
+                    (*r.norm_apply(y, y, pos, w, w), *r.norm_backward(y, y, y, y, pos, w, w)[:2])):
+        # one rounding on each side, and float32 sums in two orders: test_gpu_layers.py has 2^-19 of a vector's size for one
+        # (of y forward; of r |t w| in the gradient, at most sqrt(2) max|x| max|w| max r = 22 here)
+        size = (b.double().abs().amax(-1, keepdim=True) + 22).cpu()
+        off = (a.double() - b.double()).abs().cpu() - 2 * torch.finfo(dtype).eps / 2 * b.double().abs().cpu() - 2.0 ** -18 * size
+        assert float(off.max()) <= 0
+    for a, b in zip((*att.forward(x, x, x, **one), *att.backward(x, x, x, x, **one)),
+                    (*att.forward(y, y, y, **one), *att.backward(y, y, y, y, **one))):
+        assert torch.equal(a, b)
+    states = [rnd(4, T, H, d, d).cuda() for _ in range(2)]
+    assert torch.equal(att.step(x, x, x, states[0]), att.step(y, y, y, states[1]))
+    assert torch.equal(*states)
