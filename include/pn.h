@@ -353,7 +353,8 @@ PN_API pn_status pn_activation(int which, const float* x, float* y, long long n,
  *    data[b batch_stride + t token_stride + h head_stride + j] (strides in
  *    elements, >= 0, rows contiguous).  16-byte aligned data and strides that
  *    are multiples of 16 bytes run fastest; any others are correct.  Outputs
- *    must not overlap each other or, except where said, inputs.
+ *    must not overlap themselves, each other or, except where said, inputs; outputs whose
+ *    rows overlap and outputs that begin where another array does are refused.
  *  - Workspaces are the caller's (16-byte aligned device memory of at least the
  *    size that the query returns for the same shape); a call leaves nothing in
  *    one for the next call.  Calls that may overlap need one each.
@@ -405,7 +406,7 @@ PN_API void pn_rotary_destroy(pn_rotary r);
  *   B, T       batch entries and tokens of each; Hq, Hk heads; dim even, <= 256
  *   positions  device [B][T], any int64
  *   inverse    1: by the opposite angles (times m): the gradient of inverse = 0
- *   q_out, k_out  may be q and k themselves (the same data and strides) */
+ *   q_out, k_out  may be q and k themselves (the same data and strides; not each other's) */
 PN_API pn_status pn_rotary_apply(pn_rotary r, int dtype, int B, int T, int Hq, int Hk, int dim,
                                  const pn_heads* q, const pn_heads* k, const long long* positions,
                                  int inverse, const pn_heads* q_out, const pn_heads* k_out,

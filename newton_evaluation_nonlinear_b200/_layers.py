@@ -98,11 +98,11 @@ def _heads(name, t, like, heads, dim):
 
 
 def _output(name, t, like, heads, dim):
-    """The same of an output: tensors whose elements share memory (expanded ones) are refused."""
+    """The same of an output: tensors whose rows overlap (expanded ones, windows) are refused."""
     row = _heads(name, t, like, heads, dim)
-    if 0 in row[1:]:
-        for n, s in zip(t.shape, t.stride()):
-            if n > 1 and s == 0:
+    if min(row[1:]) < dim:
+        for n, s in zip(t.shape[:-1], t.stride()):
+            if n > 1 and s < dim:
                 raise ValueError(f"{name} has overlapping elements")
     return row
 
@@ -241,7 +241,7 @@ class Rotary:
 
     def apply(self, q, k, positions, out=None):
         """(q, k) rotated.  positions: int64, the shape of q without heads and dim.  ``out``: a pair of tensors, which may
-        be (q, k) themselves."""
+        be (q, k) themselves and must overlap nothing else of the call."""
         return self._rotate(q, k, positions, out, 0)
 
     def apply_backward(self, dq, dk, positions, out=None):
@@ -261,7 +261,8 @@ class Rotary:
         return out
 
     def norm_backward(self, dq_out, dk_out, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
-        """(dq, dk, dwq, dwk) of :meth:`norm_apply`; dwq and dwk are float32 [dim].  ``out`` may be (dq_out, dk_out)."""
+        """(dq, dk, dwq, dwk) of :meth:`norm_apply`; dwq and dwk are float32 [dim].  ``out`` may be (dq_out, dk_out) and must
+        overlap nothing else of the call."""
         import torch
         like, K, hq, hk, pos = self._operands(q, k, positions)
         _, B, T, H, d, _, device = like
@@ -346,7 +347,7 @@ class LinearAttention:
         q [batch, tokens, heads, dk], k and v with kv_heads; or, with ``cu_seqlens`` (int32 [sequences + 1], on the
         device), packed [rows, heads, dk], where rows before the first and behind the last sequence are neither read nor
         written.  ``max_len``: the longest sequence, a hint for the work's split.  States: float32
-        [sequences, heads, dk, dv].  ``out``: a tensor for o."""
+        [sequences, heads, dk, dv].  ``out``: a tensor for o, which overlaps no input."""
         import torch
         like, hq, hk, hv = self._operands(q, k, v)
         n, T, cu, max_len = self._sequences(like, cu_seqlens, max_len)
@@ -367,7 +368,8 @@ class LinearAttention:
     def backward(self, do, q, k, v, initial_state=None, dstate=None, cu_seqlens=None, max_len: Optional[int] = None,
                  grads=None):
         """(dq, dk, dv, gradient of the initial state) of :meth:`forward` with the same inputs, from the gradients of o
-        and (None: zero) of the final state.  ``grads``: a triple of tensors for dq, dk and dv."""
+        and (None: zero) of the final state.  ``grads``: a triple of tensors for dq, dk and dv, which overlap neither each
+        other nor an input."""
         import torch
         like, hq, hk, hv = self._operands(q, k, v)
         n, T, cu, max_len = self._sequences(like, cu_seqlens, max_len)
@@ -401,7 +403,7 @@ class LinearAttention:
 
         q [rows, heads, dk], k and v with kv_heads.  ``slots``: int64 [rows], the state of each row (None: row b has
         state b); a slot outside the states, or one that an earlier row names, makes its row padding, which is left as it
-        is (in ``out`` too; without ``out`` such rows are undefined).  ``wq``, ``wk``: the norm of q and k, ``rotary``
+        is (in ``out`` too, which overlaps no other argument; without ``out`` such rows are undefined).  ``wq``, ``wk``: the norm of q and k, ``rotary``
         with ``positions`` (int64 [rows]): their rotation, both in the same pass."""
         import torch
         if q.dim() != 3:

@@ -59,6 +59,17 @@ pn_status seq_device(const void* p, const char* name, int* dev) {
   return PN_OK;
 }
 
+pn_status seq_output(const pn_heads* y, const char* name, long long B, long long T, int H, int dim) {
+  if ((B > 1 && y->batch_stride < dim) || (T > 1 && y->token_stride < dim) || (H > 1 && y->head_stride < dim))
+    return seq_fail(PN_ERR_INVALID, "%s has overlapping rows", name);
+  return PN_OK;
+}
+
+pn_status seq_apart(const void* y, const char* name, const void* x, const char* other) {
+  if (y == x) return seq_fail(PN_ERR_INVALID, "%s is the memory of %s", name, other);
+  return PN_OK;
+}
+
 namespace {
 
 struct HeadsArgs {
@@ -529,6 +540,18 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
   }
   for (int i = 0; i < (grad ? 6 : 4) && rows > 0; ++i)
     if ((uintptr_t)every[i]->data % dtype_size(dtype)) return seq_fail(PN_ERR_INVALID, "%s is misaligned", names[i]);
+  for (int o = 2; o < 4 && rows > 0; ++o) {   // an output may be the input or the gradient that it takes the place of, no other array
+    const int H = o == 2 ? Hq : Hk;
+    if (pn_status e = seq_output(every[o], names[o], B, T, H, dim)) return e;
+    for (int i = 0; i < (grad ? 6 : 4); ++i) {
+      if (i == o) continue;
+      const bool in_place = (i & 1) == (o & 1) && (B == 1 || every[i]->batch_stride == every[o]->batch_stride) &&
+                            (T == 1 || every[i]->token_stride == every[o]->token_stride) &&
+                            (H == 1 || every[i]->head_stride == every[o]->head_stride);
+      if (in_place) continue;
+      if (pn_status e = seq_apart(every[o]->data, names[o], every[i]->data, names[i])) return e;
+    }
+  }
   if (rows == 0 && !grad) return PN_OK;
   SeqDeviceGuard dg(dev);
   if (rows == 0) {

@@ -280,6 +280,11 @@ pn_status pn_linattn_forward(pn_linattn h, int n_seq, long long T, const int* cu
   if (pn_status e = check_f32(final_state, "final_state", &dev)) return e;
   if (cu_seqlens)
     if (pn_status e = seq_device(cu_seqlens, "cu_seqlens", &dev)) return e;
+  if (!empty) {
+    if (pn_status e = seq_output(o, "o", cu_seqlens ? 1 : n_seq, T, h->H, h->dv)) return e;
+    for (int i = 0; i < 3; ++i)
+      if (pn_status e = seq_apart(o->data, "o", ops[i]->data, names[i])) return e;
+  }
   if (n_seq == 0 || (empty && !final_state)) return PN_OK;
   const size_t need = pn_linattn_workspace(h, 0, n_seq, T, cu_seqlens != nullptr, max_len);
   if (workspace_bytes < need) return seq_fail(PN_ERR_INVALID, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -330,6 +335,11 @@ pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const int* c
   if (pn_status e = check_f32(d_initial_state, "d_initial_state", &dev)) return e;
   if (cu_seqlens)
     if (pn_status e = seq_device(cu_seqlens, "cu_seqlens", &dev)) return e;
+  for (int o = 4; o < 7 && !empty; ++o) {
+    if (pn_status e = seq_output(ops[o], names[o], cu_seqlens ? 1 : n_seq, T, o == 4 ? h->H : h->Hkv, o == 6 ? h->dv : h->dk)) return e;
+    for (int i = 0; i < o; ++i)
+      if (pn_status e = seq_apart(ops[o]->data, names[o], ops[i]->data, names[i])) return e;
+  }
   if (n_seq == 0 || (empty && !d_initial_state)) return PN_OK;
   const size_t need = pn_linattn_workspace(h, 1, n_seq, T, cu_seqlens != nullptr, max_len);
   if (workspace_bytes < need) return seq_fail(PN_ERR_INVALID, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -436,6 +446,10 @@ pn_status pn_linattn_step(pn_linattn h, int rows, const pn_heads* q, const pn_he
     if (pn_status e = seq_device(wq, "wq", &dev)) return e;
     if (pn_status e = seq_device(wk, "wk", &dev)) return e;
   }
+  if (pn_status e = seq_output(o, "o", rows, 1, h->H, h->dv)) return e;
+  for (int i = 0; i < 3; ++i)
+    if (pn_status e = seq_apart(o->data, "o", ops[i]->data, names[i])) return e;
+  if (pn_status e = seq_apart(o->data, "o", states, "states")) return e;
   SeqDeviceGuard dg(dev);
   const int G = h->H / h->Hkv;
   LinStep P = {};

@@ -32,6 +32,10 @@ void set_thread_error(const char* msg);   // pn_api.cu: the text of pn_last_erro
 pn_status seq_fail(pn_status st, const char* fmt, ...);
 // Device of a device (or managed) pointer; *dev < 0 takes that device, else it must match.
 pn_status seq_device(const void* p, const char* name, int* dev);
+// Refuses an output [B][T][H] of rows of dim elements that overlap each other.
+pn_status seq_output(const pn_heads* y, const char* name, long long B, long long T, int H, int dim);
+// Refuses an output that is the memory of another array of the call (arrays that overlap in part are the caller's care).
+pn_status seq_apart(const void* y, const char* name, const void* x, const char* other);
 inline size_t dtype_size(int dtype) { return dtype == PN_F32 ? 4 : 2; }
 
 // Restores the caller's current device on scope exit.

@@ -163,3 +163,69 @@ def test_windows_that_overlap(dtype):
     states = [rnd(4, T, H, d, d).cuda() for _ in range(2)]
     assert torch.equal(att.step(x, x, x, states[0]), att.step(y, y, y, states[1]))
     assert torch.equal(*states)
+
+
+def test_outputs_in_the_place_of_other_arrays_are_refused():
+    """Where a pass would read what it has overwritten.  Rotations and norms may write over what they replace, no further."""
+    T, H, d = 8, 2, 64
+    r, att = pn.Rotary(d), pn.LinearAttention(H, H, d, d, [-0.1] * H)
+    q, k, v, do = (rnd(i, T, H, d).cuda() for i in range(4))
+    pos, w = torch.arange(T, device="cuda"), torch.ones(d, device="cuda")
+    e = lambda: torch.empty_like(q)  # noqa: E731
+    for out in [(k, q), (q, q), (e(), q), (k, e())]:
+        with pytest.raises(pn.PnError, match="memory"):
+            r.apply(q, k, pos, out=out)
+        with pytest.raises(pn.PnError, match="memory"):
+            r.norm_apply(q, k, pos, w, w, out=out)
+        with pytest.raises(pn.PnError, match="memory"):
+            r.norm_backward(q, k, do, v, pos, w, w, out=out)
+    long = torch.zeros(2 * T, H, d, device="cuda")
+    with pytest.raises(pn.PnError, match="memory"):   # in place, but with other strides
+        r.apply(long[::2], k, pos, out=(long[:T], e()))
+    for out in (q, k, v):
+        with pytest.raises(pn.PnError, match="memory"):
+            att.forward(q[None], k[None], v[None], out=out[None])
+        with pytest.raises(pn.PnError, match="memory"):
+            att.step(q, k, v, torch.zeros(T, H, d, d, device="cuda"), out=out)
+    both = torch.zeros(T, H, d, d, device="cuda")
+    with pytest.raises(pn.PnError, match="memory"):
+        att.step(q, k, v, both, out=both.view(-1)[: T * H * d].view(T, H, d))
+    for grads in [(q, e(), e()), (e(), k, e()), (e(), e(), do)] + [(k, e(), e())]:
+        with pytest.raises(pn.PnError, match="memory"):
+            att.backward(do[None], q[None], k[None], v[None], grads=tuple(x[None] for x in grads))
+    one = e()
+    with pytest.raises(pn.PnError, match="memory"):
+        att.backward(do[None], q[None], k[None], v[None], grads=(one[None], e()[None], one[None]))
+    windows = torch.zeros(T * H * d, device="cuda").as_strided((T, H, d), (d, 8, 1))
+    with pytest.raises(ValueError, match="overlapping"):
+        r.apply(q, k, pos, out=(windows, e()))
+    with pytest.raises(ValueError, match="overlapping"):
+        att.forward(q[None], k[None], v[None], out=windows[None])
+    h = lambda t: pn.pn_heads(t.data_ptr(), 0, t.stride(0), t.stride(1))  # noqa: E731
+    assert pn.lib.pn_rotary_apply(r.h, pn.PN_F32, 1, T, H, H, d, h(q), h(k), pos.data_ptr(), 0, h(windows), h(e()),
+                                  None) == pn.PN_ERR_INVALID
+    assert "overlapping" in pn.pn_last_error(None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_in_place_gradients(dtype):
+    """apply_backward over the gradients it takes, norm_backward over those or over the inputs: the same bits."""
+    T, H, K, d = 300, 4, 2, 64
+    r = pn.Rotary(d)
+    q, k, gq, gk = (rnd(i, T, n, d, dtype=dtype).cuda() for i, n in ((1, H), (2, K), (3, H), (4, K)))
+    pos, w = torch.arange(T, device="cuda"), rnd(5, d).cuda()
+    want = r.apply_backward(gq, gk, pos)
+    a, b = gq.clone(), gk.clone()
+    r.apply_backward(a, b, pos, out=(a, b))
+    assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    want = r.norm_backward(gq, gk, q, k, pos, w, w)
+    a, b = gq.clone(), gk.clone()
+    for x, y in zip(r.norm_backward(a, b, q, k, pos, w, w, out=(a, b)), want):
+        assert torch.equal(x, y)
+    a, b = q.clone(), k.clone()
+    for x, y in zip(r.norm_backward(gq, gk, a, b, pos, w, w, out=(a, b)), want):
+        assert torch.equal(x, y)
+    # the gradients side by side in one buffer, as one projection's gradient wants them
+    both = torch.zeros(T, H + K, d, dtype=dtype, device="cuda")
+    r.norm_backward(gq, gk, q, k, pos, w, w, out=(both[:, :H], both[:, H:]))
+    assert torch.equal(both[:, :H], want[0]) and torch.equal(both[:, H:], want[1])
