@@ -184,7 +184,8 @@ class Rotary:
               (per frequency, by its turns over ``original_length``)
     attention_scale   factor on the rotated elements; None: 1, or 0.1 ln(factor) + 1 for "yarn"
 
-    The plan holds no device memory; one object serves every device and stream.
+    The plan holds no device memory; one object serves every device and stream.  Copies, pickled ones too, are plans of
+    their own.
     """
 
     def __init__(self, rot_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
@@ -203,6 +204,10 @@ class Rotary:
         h = ctypes.c_void_p()
         _ok(lib.pn_rotary_create(ctypes.byref(h), ctypes.byref(desc)))
         self.h = h.value
+        self._args = (rot_dim, base, layout, scaling, factor, original_length, beta_fast, beta_slow, attention_scale)
+
+    def __reduce__(self):   # (a copy of the address alone would be destroyed twice)
+        return type(self), self._args
 
     def __del__(self):
         try:
@@ -287,6 +292,8 @@ class LinearAttention:
     log_decay         [heads], finite and <= 0, on the host or a device (read once, here; no gradient is formed for it)
     scale             None: dk ** -0.5
     dtype             of q, k, v and o: torch.float32, bfloat16 or float16; states are float32
+
+    Copies, pickled ones too, are handles of their own.
     """
 
     def __init__(self, heads: int, kv_heads: int, dk: int, dv: int, log_decay, scale: Optional[float] = None, dtype=None):
@@ -308,6 +315,10 @@ class LinearAttention:
         _ok(lib.pn_linattn_create(ctypes.byref(h), self.heads, self.kv_heads, self.dk, self.dv, _dtypes()[self.dtype],
                                   g.ctypes.data, self.scale))
         self.h = h.value
+        self._args = (self.heads, self.kv_heads, self.dk, self.dv, g.copy(), self.scale, self.dtype)
+
+    def __reduce__(self):   # (a copy of the address alone would be destroyed twice)
+        return type(self), self._args
 
     def __del__(self):
         try:
