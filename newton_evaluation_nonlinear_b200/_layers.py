@@ -3,7 +3,8 @@
 :class:`Rotary` rotates queries and keys by position, with or without the norm of each head vector before it;
 :class:`LinearAttention` is the recurrence S_t = exp(g_h) S_{t-1} + k_t v_t^T, o_t = scale q_t S_t, over whole prompts
 and for single tokens.  Gradients are explicit calls (``apply_backward``, ``norm_backward``, ``backward``); results
-carry no autograd graph.
+carry no autograd graph, so tensors that require a gradient are refused while torch records one: call from a
+torch.autograd.Function, under torch.no_grad(), or with detached tensors.
 
 Tensors are [tokens, heads, dim] or [batch, tokens, heads, dim], CUDA, of one of the types float32, bfloat16 and
 float16, with contiguous rows and any other strides (slices of one projection's output go in as they are).  The work
@@ -60,6 +61,16 @@ def _dtype(name, t):
 def _ok(status: int) -> None:
     if status != PN_OK:
         raise PnError(status, pn_last_error(None))
+
+
+def _no_graph(*tensors):
+    """Refuses tensors whose gradients torch would expect to be recorded."""
+    import torch
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("a tensor requires a gradient, which this call does not record: call it under torch.no_grad() "
+                                 "or from a torch.autograd.Function, or detach the tensor")
 
 
 def _first(name, t):
@@ -236,6 +247,7 @@ class Rotary:
         return (oq, ok), _output("out[0]", oq, like, H, d), _output("out[1]", ok, like, K, d)
 
     def _rotate(self, q, k, positions, out, inverse):
+        _no_graph(q, k, *(out or ()))
         like, K, hq, hk, pos = self._operands(q, k, positions)
         _, B, T, H, d, _, device = like
         out, oq, ok = self._out(q, k, like, K, out)
@@ -256,6 +268,7 @@ class Rotary:
     def norm_apply(self, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
         """x_j w_j / sqrt(mean(x^2) + eps) of each head vector, then the rotation, in one pass.  The weights are [dim],
         float32 or of the queries' type."""
+        _no_graph(q, k, wq, wk, *(out or ()))
         like, K, hq, hk, pos = self._operands(q, k, positions)
         _, B, T, H, d, _, device = like
         w = _weights(wq, wk, d, device)
@@ -269,6 +282,7 @@ class Rotary:
         """(dq, dk, dwq, dwk) of :meth:`norm_apply`; dwq and dwk are float32 [dim].  ``out`` may be (dq_out, dk_out) and must
         overlap nothing else of the call."""
         import torch
+        _no_graph(dq_out, dk_out, q, k, wq, wk, *(out or ()))
         like, K, hq, hk, pos = self._operands(q, k, positions)
         _, B, T, H, d, _, device = like
         gq, gk = _heads("dq_out", dq_out, like, H, d), _heads("dk_out", dk_out, like, K, d)
@@ -360,6 +374,7 @@ class LinearAttention:
         written.  ``max_len``: the longest sequence, a hint for the work's split.  States: float32
         [sequences, heads, dk, dv].  ``out``: a tensor for o, which overlaps no input."""
         import torch
+        _no_graph(q, k, v, initial_state, out)
         like, hq, hk, hv = self._operands(q, k, v)
         n, T, cu, max_len = self._sequences(like, cu_seqlens, max_len)
         shape, device = (n, self.heads, self.dk, self.dv), like[-1]
@@ -382,6 +397,7 @@ class LinearAttention:
         and (None: zero) of the final state.  ``grads``: a triple of tensors for dq, dk and dv, which overlap neither each
         other nor an input."""
         import torch
+        _no_graph(do, q, k, v, initial_state, dstate, *(grads or ()))
         like, hq, hk, hv = self._operands(q, k, v)
         n, T, cu, max_len = self._sequences(like, cu_seqlens, max_len)
         shape, device = (n, self.heads, self.dk, self.dv), like[-1]
@@ -417,6 +433,7 @@ class LinearAttention:
         is (in ``out`` too, which overlaps no other argument; without ``out`` such rows are undefined).  ``wq``, ``wk``: the norm of q and k, ``rotary``
         with ``positions`` (int64 [rows]): their rotation, both in the same pass."""
         import torch
+        _no_graph(q, k, v, states, wq, wk, out)
         if q.dim() != 3:
             raise ValueError("q must be [rows, heads, dk]")
         like, hq, hk, hv = self._operands(q, k, v)

@@ -26,3 +26,33 @@ def test_copies_are_handles_of_their_own(make):
     assert pn.lib.pn_linattn_workspace(b.h, 1, 2, 4096, 0, 0) > 0
     both = make([b, s, b])
     del both, s, b
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    """Results carry no graph: while torch records one, an argument that requires a gradient would lose it in silence.  (The
+    refusal comes first; the same calls without recording go on to the next check, that of the device.)"""
+    r, att = pn.Rotary(8), pn.LinearAttention(2, 2, 8, 8, [0.0, -0.1])
+    x, w, pos = torch.zeros(1, 3, 2, 8), torch.ones(8), torch.zeros(1, 3, dtype=torch.int64)
+    s = torch.zeros(3, 2, 8, 8)
+    calls = [(r.apply, dict(q=x, k=x, positions=pos), "q k"), (r.apply_backward, dict(dq=x, dk=x, positions=pos), "dq dk"),
+             (r.norm_apply, dict(q=x, k=x, positions=pos, wq=w, wk=w), "q k wq wk"),
+             (r.norm_backward, dict(dq_out=x, dk_out=x, q=x, k=x, positions=pos, wq=w, wk=w), "dq_out dk_out q k wq wk"),
+             (att.forward, dict(q=x, k=x, v=x, initial_state=s[:1], out=x), "q k v initial_state out"),
+             (att.backward, dict(do=x, q=x, k=x, v=x, initial_state=s[:1], dstate=s[:1]), "do q k v initial_state dstate"),
+             (att.step, dict(q=x[0], k=x[0], v=x[0], states=s, wq=w, wk=w), "q k v states wq wk")]
+    for call, kw, names in calls:
+        for name in names.split():
+            leaf = kw[name].clone().requires_grad_()
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(**{**kw, name: leaf})
+            with pytest.raises(ValueError, match="requires a gradient"):
+                call(**{**kw, name: leaf * 1})
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+                call(**{**kw, name: leaf})
+        with pytest.raises(ValueError, match="CUDA"):
+            call(**kw)
+    for call, kw, key in ((r.apply, calls[0][1], "out"), (r.norm_backward, calls[3][1], "out")):
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call(**kw, **{key: (x, x.clone().requires_grad_())})
+    with pytest.raises(ValueError, match="requires a gradient"):
+        att.backward(x, x, x, x, grads=(x, x, x.clone().requires_grad_()))
