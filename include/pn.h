@@ -347,8 +347,9 @@ PN_API pn_status pn_activation(int which, const float* x, float* y, long long n,
  *    returns without waiting.  They allocate nothing on the device and can be
  *    captured into a CUDA graph.  Device and pinned memory must stay alive
  *    until the stream has run the work.
- *  - Plans and handles hold host memory only and never change after creation:
- *    one may serve any device, stream and thread, several at once.
+ *  - Plans and handles hold host memory only and never change after creation
+ *    (but by pn_linattn_debug_waits): one may serve any device, stream and
+ *    thread, several at once.
  *  - Rows of heads are pn_heads: element (b, t, h, j) is at
  *    data[b batch_stride + t token_stride + h head_stride + j] (strides in
  *    elements, >= 0, rows contiguous).  16-byte aligned data and strides that
@@ -486,10 +487,16 @@ PN_API pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const
                                      size_t workspace_bytes, void* cuda_stream);
 
 /* Waits for the stream, then reports whether a bounded device wait of pn_linattn_forward or
- * pn_linattn_backward on the current device has given up since the last check (PN_ERR_TIMEOUT: what those
- * calls wrote is invalid; the report is cleared).  No call is known to do so; the calls themselves do not wait
- * and cannot tell. */
+ * pn_linattn_backward on the current device, in any stream, has given up since the last check of this stream
+ * there (PN_ERR_TIMEOUT: what those calls wrote is invalid).  One stream's check takes no report from
+ * another's; of two streams both are told.  No call is known to give up; the calls themselves do not wait and
+ * cannot tell. */
 PN_API pn_status pn_linattn_check(void* cuda_stream);
+
+/* Test hook: the limit on each of those waits in later calls with this handle (in nanoseconds, 1000 to 4e9;
+ * 2e9 by default), and a chunk of 64 rows from which on none is loaded in any part of a sequence, so that the
+ * waits for them run out (-1: all are, the default).  Not while another thread uses the handle. */
+PN_API pn_status pn_linattn_debug_waits(pn_linattn h, long long timeout_ns, int stall_chunk);
 
 /* One token of each of `rows` (<= 65535) sequences, in one launch: the states are updated in place.
  *   q, k, v, o  row b at batch_stride (token_stride ignored)

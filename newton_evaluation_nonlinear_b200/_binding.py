@@ -102,6 +102,7 @@ SIGNATURES = {
     "pn_linattn_backward": (_c_int, [_vp, _c_int, _c_ll, _vp, _c_ll] + [_heads] * 4 + [_vp, _vp] + [_heads] * 3
                             + [_vp, _vp, _c_size, _vp]),
     "pn_linattn_check": (_c_int, [_vp]),
+    "pn_linattn_debug_waits": (_c_int, [_vp, _c_ll, _c_int]),
     "pn_linattn_step": (_c_int, [_vp, _c_int] + [_heads] * 4 + [_vp, _c_ll, _vp, _vp, _vp, _vp, _vp, _c_int,
                                                                _c_float, _vp]),
     "pn_last_error": (ctypes.c_char_p, [_vp]),

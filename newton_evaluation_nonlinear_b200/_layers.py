@@ -418,8 +418,9 @@ class LinearAttention:
 
     @staticmethod
     def check(device=None):
-        """Wait for the current stream and raise where a bounded device wait of a forward or backward pass on the device has
-        given up since the last check (its results are invalid).  The passes are asynchronous and cannot tell."""
+        """Wait for the current stream and raise where a bounded device wait of a forward or backward pass on the device, in any
+        stream, has given up since the last check of this stream (results are invalid).  The passes are asynchronous and
+        cannot tell."""
         import torch
         with torch.cuda.device(device):
             _ok(lib.pn_linattn_check(torch.cuda.current_stream().cuda_stream))

@@ -1,7 +1,11 @@
 // pn_linattn.cu -- entry points of linear attention with a decay for each head.
 #include <algorithm>
 #include <cmath>
+#include <exception>
+#include <map>
 #include <memory>
+#include <mutex>
+#include <utility>
 
 #include "pn_linattn_tc.cuh"
 
@@ -159,6 +163,8 @@ bool try_tc(const pn_linattn_s* h, LinPass& P, const LinDecay& G, long long max_
   P.nseg = tc_parts(h, P.n_seq, max_len, P.dc);
   using T = __nv_bfloat16;
   const bool narrow = tc_columns(h, P.n_seq, P.dc) == 64;
+  P.wait_ns = h->wait_ns;
+  P.stall = h->stall;
   P.by_length = tc_by_length(h, P, max_len, narrow ? 64 : 128);
   if (P.da <= 64) *e = narrow ? launch_tc<T, 64, 64>(maps, P, G, st) : launch_tc<T, 64, 128>(maps, P, G, st);
   else *e = narrow ? launch_tc<T, 128, 64>(maps, P, G, st) : launch_tc<T, 128, 128>(maps, P, G, st);
@@ -246,6 +252,8 @@ pn_status pn_linattn_create(pn_linattn* out, int H, int Hkv, int dk, int dv, int
   h->dv = dv;
   h->dtype = dtype;
   h->scale = scale;
+  h->wait_ns = kLinWaitNs;
+  h->stall = -1;
   // (2^-1e30 is zero as well, and its multiples by zero are zero: an infinite exponent's are not)
   for (int i = 0; i < H; ++i) h->log2_decay[i] = (float)std::max((double)log_decay[i] * 1.4426950408889634074, -1e30);
   *out = h;
@@ -406,15 +414,38 @@ pn_status pn_linattn_backward(pn_linattn h, int n_seq, long long T, const int* c
   return PN_OK;
 }
 
+pn_status pn_linattn_debug_waits(pn_linattn h, long long timeout_ns, int stall_chunk) {
+  if (!h) return seq_fail(PN_ERR_INVALID, "handle is NULL");
+  if (timeout_ns < 1000 || timeout_ns > 4000000000LL) return seq_fail(PN_ERR_INVALID, "timeout: from 1000 to 4e9 ns");
+  if (stall_chunk < -1) return seq_fail(PN_ERR_INVALID, "stall_chunk must be >= -1");
+  h->wait_ns = (unsigned)timeout_ns;
+  h->stall = stall_chunk;
+  return PN_OK;
+}
+
 pn_status pn_linattn_check(void* cuda_stream) {
+  // what each (device, stream) has been told of so far
+  static std::mutex lock;
+  static std::map<std::pair<int, void*>, unsigned> told;
   cudaStream_t st = (cudaStream_t)cuda_stream;
-  unsigned word = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&word, lin_error_word, sizeof word, 0, cudaMemcpyDeviceToHost, st);
+  unsigned count = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&count, lin_gave_up, sizeof count, 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  if (e == cudaSuccess && word) e = cudaMemcpyToSymbolAsync(lin_error_word, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, st);
-  if (e == cudaSuccess && word) e = cudaStreamSynchronize(st);
-  if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "reading the device's error word failed: %s", cudaGetErrorString(e));
-  if (word) return seq_fail(PN_ERR_TIMEOUT, "a device wait of linear attention gave up: results since the last check are invalid");
+  if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "reading the device's count of waits failed: %s", cudaGetErrorString(e));
+  unsigned before;
+  try {
+    std::lock_guard<std::mutex> g(lock);
+    unsigned& seen = told[{dev, cuda_stream}];
+    before = seen;
+    // (a check of this stream in another thread may have read a later count)
+    if ((int)(count - before) > 0) seen = count;
+  } catch (const std::exception&) {
+    return seq_fail(PN_ERR_NOMEM, "out of host memory");
+  }
+  if ((int)(count - before) > 0)
+    return seq_fail(PN_ERR_TIMEOUT, "a device wait of linear attention gave up: results since the last check are invalid");
   return PN_OK;
 }
 

@@ -21,6 +21,8 @@ struct pn_linattn_s {
   int H, Hkv, dk, dv, dtype;
   float scale;
   float log2_decay[kMaxLinHeads];
+  unsigned wait_ns;    // limit of each device wait
+  int stall;           // test hook: from this chunk of each part on none is loaded (-1: all are)
 };
 
 namespace pn {
@@ -37,6 +39,8 @@ struct LinPass {
   long long out_bs, out_ts, out_hs;
   int out_f32;             // out is float32 (partial gradients of shared heads)
   int out_map;             // whole chunks of out are stored by TMA
+  unsigned wait_ns;        // limit of a device wait
+  int stall;               // test hook: from this chunk of each part on none is loaded (-1: all are)
   int by_length;           // sequences are taken longest first
   int vec;                 // every row of the four arrays is aligned to four elements
   int da, dc;              // widths: a and b, c and out

@@ -57,10 +57,10 @@
 
 namespace pn {
 
-// Set by a wait that gave up (see pn_linattn_check).
-__device__ unsigned lin_error_word;
+// Waits that gave up on this device, ever (see pn_linattn_check): never cleared, so that nobody's report is taken by another.
+__device__ unsigned lin_gave_up;
 
-constexpr long long kLinWaitNs = 2000000000LL;
+constexpr unsigned kLinWaitNs = 2000000000u;   // the limit where the handle sets none, and of the closing waits
 
 // A try that the hardware may keep asleep for up to 20 us.
 __device__ __forceinline__ bool lin_try(uint64_t* bar, unsigned parity) {
@@ -74,19 +74,23 @@ __device__ __forceinline__ bool lin_try(uint64_t* bar, unsigned parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait; gives up when the CTA has been told to, or after kLinWaitNs.
-__device__ __forceinline__ bool lin_wait(uint64_t* bar, unsigned parity, volatile int* abort) {
+// Bounded wait; gives up when the CTA has been told to, or after P.wait_ns.
+__device__ __forceinline__ bool lin_wait(uint64_t* bar, unsigned parity, volatile int* abort, const LinPass& P) {
   if (lin_try(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer();
+  const unsigned t0 = (unsigned)globaltimer();
   while (true) {
     if (lin_try(bar, parity)) return true;
     if (*abort) return false;
-    if ((long long)(globaltimer() - t0) > kLinWaitNs) {
-      atomicExch(&lin_error_word, 1u);
+    if ((unsigned)globaltimer() - t0 > P.wait_ns) {
+      atomicAdd(&lin_gave_up, 1u);
       *abort = 1;
       return false;
     }
   }
+}
+// Waits for what the CTA has in flight before it ends.
+__device__ __forceinline__ void lin_drain(uint64_t* bar, unsigned parity) {
+  if (!mbar_drain(bar, parity, kLinWaitNs)) atomicAdd(&lin_gave_up, 1u);
 }
 
 // Instruction descriptor for kind::f16: D fp32, A and B of one 16-bit type (0: f16, 1: bf16),
@@ -460,10 +464,11 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       // ------------------------------- loads -------------------------------
       if (lane == 0) {
         const int bz = P.cu ? 0 : s;
-        for (int m = 0; m < M; ++m) {
+        const int loads = (int)min((unsigned)M, (unsigned)P.stall);   // (all; a test may leave out the rest, and the waits for them run out)
+        for (int m = 0; m < loads; ++m) {
           const int st = m % NS;
-          if (m == 1 && !lin_wait(&bar_init, 0u, &s_abort)) break;   // the state came in by way of the other stages
-          if (m >= NS && !lin_wait(&bar_empty[st], (unsigned)(m / NS - 1) & 1u, &s_abort)) break;
+          if (m == 1 && !lin_wait(&bar_init, 0u, &s_abort, P)) break;   // the state came in by way of the other stages
+          if (m >= NS && !lin_wait(&bar_empty[st], (unsigned)(m / NS - 1) & 1u, &s_abort, P)) break;
           const int row = (int)start + chunk_of(m) * C;
           mbar_arrive_expect_tx(&bar_full[st], (unsigned)(STATE_ONLY ? K::STAGE - K::A_BYTES : K::STAGE));
 #pragma unroll
@@ -507,8 +512,8 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       for (int m = 0; m < M && ok && warp == 1; ++m) {
         const int st = m % NS;
         // what the chunk adds to the state, once what the chunk before added is read
-        if (!(ok = lin_wait(&bar_cp[m & 1], (unsigned)(m >> 1) & 1u, &s_abort))) break;
-        if (m > 0 && !(ok = lin_wait(&bar_ur, (unsigned)(m - 1) & 1u, &s_abort))) break;
+        if (!(ok = lin_wait(&bar_cp[m & 1], (unsigned)(m >> 1) & 1u, &s_abort, P))) break;
+        if (m > 0 && !(ok = lin_wait(&bar_ur, (unsigned)(m - 1) & 1u, &s_abort, P))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t db = mnmaj(sB(st));
@@ -532,10 +537,10 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       // the outputs: the state's share and the chunk's own, once what their columns held is read
       for (int m = 0; m < M && ok && warp == 2 && !STATE_ONLY; ++m) {
         const int st = m % NS, before = two ? m - 1 : m - 2;
-        if (!(ok = lin_wait(&bar_p[m & 1], (unsigned)(m >> 1) & 1u, &s_abort))) break;
-        if (before >= 0 && !(ok = lin_wait(&bar_o[before & 1], (unsigned)(before >> 1) & 1u, &s_abort))) break;
-        if (rows_of(m) < C && !(ok = lin_wait(&bar_zero, 0u, &s_abort))) break;
-        if (!(ok = lin_wait(&bar_s, (unsigned)m & 1u, &s_abort))) break;
+        if (!(ok = lin_wait(&bar_p[m & 1], (unsigned)(m >> 1) & 1u, &s_abort, P))) break;
+        if (before >= 0 && !(ok = lin_wait(&bar_o[before & 1], (unsigned)(before >> 1) & 1u, &s_abort, P))) break;
+        if (rows_of(m) < C && !(ok = lin_wait(&bar_zero, 0u, &s_abort, P))) break;
+        if (!(ok = lin_wait(&bar_s, (unsigned)m & 1u, &s_abort, P))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t o1 = tmem + K::COL_O + (two ? 0 : 64 * (m & 1)), o2 = tmem + K::COL_O + (two ? 64 : 64 * (m & 1));
@@ -550,8 +555,8 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       // P, once the chunk before's is read
       for (int m = 0; m < M && ok && warp == 3 && !STATE_ONLY; ++m) {
         const int st = m % NS;
-        if (!(ok = lin_wait(&bar_full[st], (unsigned)(m / NS) & 1u, &s_abort))) break;
-        if (m > 0 && !(ok = lin_wait(&bar_p[(m - 1) & 1], (unsigned)((m - 1) >> 1) & 1u, &s_abort))) break;
+        if (!(ok = lin_wait(&bar_full[st], (unsigned)(m / NS) & 1u, &s_abort, P))) break;
+        if (m > 0 && !(ok = lin_wait(&bar_p[(m - 1) & 1], (unsigned)((m - 1) >> 1) & 1u, &s_abort, P))) break;
         tc_fence_after();
         if (elect_one()) {
           product(tmem + K::COL_P, kmaj(sA(st)), Box{}, kmaj(sB(st)), Box{}, DSteps{}, id_p, false);
@@ -579,8 +584,8 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       }
       const int pi = 16 * w + mr + (mi & 1) * 8;       // row of P~ addressed; matrices: rows, rows + 8, next 8 columns
       for (int m = 0; m < M; ++m) {
-        if (m > 1 && !lin_wait(&bar_oacc[m & 1], (unsigned)((m >> 1) - 1) & 1u, &s_abort)) break;   // P~ two chunks ago is used
-        if (!lin_wait(&bar_pacc, (unsigned)m & 1u, &s_abort)) break;
+        if (m > 1 && !lin_wait(&bar_oacc[m & 1], (unsigned)((m >> 1) - 1) & 1u, &s_abort, P)) break;   // P~ two chunks ago is used
+        if (!lin_wait(&bar_pacc, (unsigned)m & 1u, &s_abort, P)) break;
         tc_fence_after();
         const int n = rows_of(m);
         unsigned char* dst = base + K::OFF_P + (m & 1) * K::P_BYTES + pi * 128;
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
       const bool wide = P.out_map || (((uintptr_t)P.out | (uintptr_t)(2 * P.out_bs) | (uintptr_t)(2 * P.out_ts) | (uintptr_t)(2 * P.out_hs)) & 15u) == 0;
       for (int m = 0; m < M; ++m) {
         unsigned char* stage = base + K::OFF_O + (K::NOUT == 2 ? (m & 1) * K::O_BYTES : 0);
-        const bool ok = lin_wait(&bar_oacc[m & 1], (unsigned)(m >> 1) & 1u, &s_abort);
+        const bool ok = lin_wait(&bar_oacc[m & 1], (unsigned)(m >> 1) & 1u, &s_abort, P);
         if (t == 0) {   // the copy that last read this memory is done with it
           if (K::NOUT == 2) bulk_wait_read_but1();
           else bulk_wait_read();
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     bool ok = true;
     for (int m = 0; m <= M; ++m) {
       if (m > 0) {
-        if (!(ok = lin_wait(&bar_u, (unsigned)(m - 1) & 1u, &s_abort))) break;
+        if (!(ok = lin_wait(&bar_u, (unsigned)(m - 1) & 1u, &s_abort, P))) break;
         tc_fence_after();
         const int n = rows_of(m - 1) - (m == 1 ? e0 - early : 0);
         const float f = n == C ? f_full : lin_pow(l2, n);
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_ur);
         // O1 of the chunk before has read S~
-        if (!STATE_ONLY && !(ok = lin_wait(&bar_o1, (unsigned)(m - 1) & 1u, &s_abort))) break;
+        if (!STATE_ONLY && !(ok = lin_wait(&bar_o1, (unsigned)(m - 1) & 1u, &s_abort, P))) break;
       }
       if (m == M) break;
       if (!STATE_ONLY) {
@@ -846,7 +851,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
     const int from = (c0 >> 6) * K::SUB + (8 * (mi >> 1) + mr) * 128 + (((((c0 & 63) >> 3) + (mi & 1)) ^ mr) << 4);
     for (int m = 0; m < M; ++m) {
       const int st = m % NS, n = rows_of(m);
-      if (!lin_wait(&bar_full[st], (unsigned)(m / NS) & 1u, &s_abort)) break;
+      if (!lin_wait(&bar_full[st], (unsigned)(m / NS) & 1u, &s_abort, P)) break;
       unsigned char* src = sC(st);
       if (n < C) {
         // Rows behind the last one hold anything: zero b and c there (the products that may be reading b
@@ -863,7 +868,7 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_zero);
       }
-      if (m > 1 && !lin_wait(&bar_cpf[m & 1], (unsigned)((m >> 1) - 1) & 1u, &s_abort)) break;   // the pieces two chunks ago are used
+      if (m > 1 && !lin_wait(&bar_cpf[m & 1], (unsigned)((m >> 1) - 1) & 1u, &s_abort, P)) break;   // the pieces two chunks ago are used
       if constexpr (K::TS) {
         __syncwarp();
 #pragma unroll 1
@@ -919,11 +924,11 @@ __global__ void __launch_bounds__(896, 1) lin_tc_kernel(const __grid_constant__ 
   __syncwarp();
   if (warp == 0 && lane == 0) {
     const int n = s_loaded;
-    for (int m = n > NS ? n - NS : 0; m < n; ++m) mbar_drain(&bar_full[m % NS], (unsigned)(m / NS) & 1u, kLinWaitNs);
+    for (int m = n > NS ? n - NS : 0; m < n; ++m) lin_drain(&bar_full[m % NS], (unsigned)(m / NS) & 1u);
   }
   if (warp >= 1 && warp <= 3) {
     if (elect_one()) umma_commit(&bar_done[warp - 1]);
-    mbar_drain(&bar_done[warp - 1], 0u, kLinWaitNs);
+    lin_drain(&bar_done[warp - 1], 0u);
   }
   tc_fence_before();
   __syncthreads();

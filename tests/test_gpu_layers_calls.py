@@ -229,3 +229,45 @@ def test_in_place_gradients(dtype):
     both = torch.zeros(T, H + K, d, dtype=dtype, device="cuda")
     r.norm_backward(gq, gk, q, k, pos, w, w, out=(both[:, :H], both[:, H:]))
     assert torch.equal(both[:, :H], want[0]) and torch.equal(both[:, H:], want[1])
+
+
+@pytest.mark.parametrize("chunk", [0, 1, 5])
+@pytest.mark.parametrize("dk, dv, n, backward", [(64, 64, 1, False), (128, 128, 1, True), (128, 64, 40, True), (64, 128, 40, False),
+                                                 (128, 128, 40, False)])
+def test_waits_that_give_up_are_reported(dk, dv, n, backward, chunk):
+    """Where a chunk is never loaded the waits for it run out after 100 us and the pass ends; every stream's check says so once,
+    and later passes are right."""
+    T, H = 2000, 2   # (n = 1: in parts of a few chunks)
+    att = pn.LinearAttention(H, H, dk, dv, [-0.01, -0.9], dtype=torch.bfloat16)
+    q, k, v, do = (rnd(i, n, T, H, w, dtype=torch.bfloat16).cuda() for i, w in enumerate((dk, dk, dv, dv)))
+    s0 = rnd(9, n, H, dk, dv).cuda()
+
+    def run():
+        return att.backward(do, q, k, v, initial_state=s0, dstate=s0) if backward else att.forward(q, k, v, initial_state=s0)
+
+    want = run()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            try:   # whatever other passes have left
+                att.check()
+            except pn.PnError:
+                pass
+            att.check()
+    assert pn.lib.pn_linattn_debug_waits(att.h, 100000, chunk if n > 1 else min(chunk, 1)) == pn.PN_OK
+    with torch.cuda.stream(streams[0]):
+        run()
+    streams[0].synchronize()
+    assert pn.lib.pn_linattn_debug_waits(att.h, 2000000000, -1) == pn.PN_OK
+    for s in reversed(streams):   # the other stream's check first: it takes nothing from this one's
+        with torch.cuda.stream(s):
+            with pytest.raises(pn.PnError) as e:
+                att.check()
+            assert e.value.status == pn.PN_ERR_TIMEOUT
+            att.check()
+    for a, b in zip(run(), want):
+        assert torch.equal(a, b)
+    for s in streams:
+        with torch.cuda.stream(s):
+            att.check()

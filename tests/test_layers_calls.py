@@ -56,3 +56,10 @@ def test_tensors_that_require_a_gradient_are_refused():
             call(**kw, **{key: (x, x.clone().requires_grad_())})
     with pytest.raises(ValueError, match="requires a gradient"):
         att.backward(x, x, x, x, grads=(x, x, x.clone().requires_grad_()))
+
+
+def test_debug_waits_refusals():
+    att = pn.LinearAttention(2, 2, 8, 8, [0.0, -0.1])
+    for args, needle in [((None, 1000, -1), "handle"), ((att.h, 999, -1), "timeout"), ((att.h, 4000000001, -1), "timeout"), ((att.h, 1000, -2), "stall_chunk")]:
+        assert pn.lib.pn_linattn_debug_waits(*args) == pn.PN_ERR_INVALID and needle in pn.pn_last_error(None)
+    assert pn.lib.pn_linattn_debug_waits(att.h, 1000, 3) == pn.PN_OK
