@@ -63,6 +63,17 @@ def _ok(status: int) -> None:
         raise PnError(status, pn_last_error(None))
 
 
+_INT = 2 ** 31 - 1
+
+
+def _int(name, n):
+    """n as the C entries' 32-bit int (ctypes would keep the low bits of a larger one)."""
+    n = int(n)
+    if not -_INT <= n <= _INT:
+        raise ValueError(f"{name}={n} does not fit 32 bits")
+    return n
+
+
 def _no_graph(*tensors):
     """Refuses tensors whose gradients torch would expect to be recorded."""
     import torch
@@ -83,6 +94,8 @@ def _first(name, t):
         B = 1
     else:
         raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    if B > _INT or T > _INT or h > _INT or d > _INT:
+        raise ValueError(f"{name} is {tuple(t.shape)}: sizes of up to 2^31 - 1 are taken")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return nd, B, T, h, d, t.dtype, t.get_device()
@@ -209,7 +222,7 @@ class Rotary:
         if attention_scale is not None and not attention_scale > 0:
             raise ValueError("attention_scale must be > 0")
         self.h = None
-        self.rot_dim = int(rot_dim)
+        self.rot_dim = _int("rot_dim", rot_dim)
         desc = pn_rotary_desc(self.rot_dim, _LAYOUTS[layout], _SCALINGS[scaling], float(base), float(factor),
                               int(original_length), float(beta_fast), float(beta_slow), float(attention_scale or 0.0))
         h = ctypes.c_void_p()
@@ -233,7 +246,7 @@ class Rotary:
         """(what k and the others are held to, key heads, rows of q and of k, address of positions)."""
         import torch
         like = nd, B, T, H, d, _, device = _first("q", q)
-        K = k.shape[-2] if k.dim() == nd else 0
+        K = _int("key heads", k.shape[-2]) if k.dim() == nd else 0
         return (like, K, _heads("q", q, like, H, d), _heads("k", k, like, K, d),
                 _ints("positions", positions, (B, T) if nd == 4 else (T,), torch.int64, device))
 
@@ -313,7 +326,8 @@ class LinearAttention:
     def __init__(self, heads: int, kv_heads: int, dk: int, dv: int, log_decay, scale: Optional[float] = None, dtype=None):
         import torch
         self.h = None
-        self.heads, self.kv_heads, self.dk, self.dv = int(heads), int(kv_heads), int(dk), int(dv)
+        self.heads, self.kv_heads = _int("heads", heads), _int("kv_heads", kv_heads)
+        self.dk, self.dv = _int("dk", dk), _int("dv", dv)
         self.dtype = torch.float32 if dtype is None else dtype
         if self.dtype not in _dtypes():
             raise ValueError(f"dtype {dtype}: float32, bfloat16 or float16 is wanted")
@@ -360,7 +374,7 @@ class LinearAttention:
             raise ValueError("packed sequences (cu_seqlens) are [tokens, heads, dim]")
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [sequences + 1]")
-        return (cu_seqlens.numel() - 1, T, _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device),
+        return (_int("sequences", cu_seqlens.numel() - 1), T, _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device),
                 int(max_len or 0))
 
     def _empty(self, q):

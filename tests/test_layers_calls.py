@@ -63,3 +63,23 @@ def test_debug_waits_refusals():
     for args, needle in [((None, 1000, -1), "handle"), ((att.h, 999, -1), "timeout"), ((att.h, 4000000001, -1), "timeout"), ((att.h, 1000, -2), "stall_chunk")]:
         assert pn.lib.pn_linattn_debug_waits(*args) == pn.PN_ERR_INVALID and needle in pn.pn_last_error(None)
     assert pn.lib.pn_linattn_debug_waits(att.h, 1000, 3) == pn.PN_OK
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """Not cut to their low bits."""
+    far = 2 ** 32 + 8
+    for make in (lambda: pn.Rotary(far), lambda: pn.LinearAttention(2, 2, far, 8, [0.0, 0.0], scale=1.0),
+                 lambda: pn.LinearAttention(2, 2, 8, far, [0.0, 0.0])):
+        with pytest.raises(ValueError, match="32 bits"):
+            make()
+    r, att = pn.Rotary(8), pn.LinearAttention(2, 2, 8, 8, [0.0, 0.0])
+    small = torch.zeros(1, 1, 1, 8)
+    for shape in ((far, 1, 1, 8), (1, far, 1, 8), (1, 1, far, 8)):
+        x = small.expand(shape)
+        pos = torch.zeros(1, 1, dtype=torch.int64).expand(shape[:2])
+        with pytest.raises(ValueError, match="2\\^31"):
+            r.apply(x, x, pos)
+        with pytest.raises(ValueError, match="2\\^31"):
+            att.forward(x, x, x)
+    with pytest.raises(ValueError, match="2\\^31"):
+        att.step(small[0].expand(far, 2, 8), small[0], small[0], torch.zeros(1, 2, 8, 8))
