@@ -683,8 +683,9 @@ pn_status pn_rotary_create(pn_rotary* out, const pn_rotary_desc* d) {
   if (d->scaling == PN_ROT_YARN &&
       (d->original_length < 1 || !(d->beta_slow >= 0.0) || !(d->beta_fast > d->beta_slow) || !std::isfinite(d->beta_fast)))
     return seq_fail(PN_ERR_INVALID, "yarn needs original_length >= 1 and beta_fast > beta_slow >= 0");
-  if (!std::isfinite(d->attention_scale) || d->attention_scale < 0.0)
-    return seq_fail(PN_ERR_INVALID, "attention_scale must be finite and >= 0");
+  if (!(d->attention_scale >= 0.0) || !std::isfinite((float)d->attention_scale) ||
+      (d->attention_scale > 0.0 && (float)d->attention_scale == 0.0f))
+    return seq_fail(PN_ERR_INVALID, "attention_scale must be finite and >= 0, as a float32 too");
   pn_rotary_plan* p = new (std::nothrow) pn_rotary_plan();
   if (!p) return seq_fail(PN_ERR_NOMEM, "out of host memory");
   p->pairs = d->rot_dim / 2;

@@ -83,3 +83,11 @@ def test_sizes_beyond_32_bits_are_refused():
             att.forward(x, x, x)
     with pytest.raises(ValueError, match="2\\^31"):
         att.step(small[0].expand(far, 2, 8), small[0], small[0], torch.zeros(1, 2, 8, 8))
+
+
+def test_attention_scales_beyond_float32_are_refused():
+    """The factor is applied as a float32: one that would become zero or infinite is refused."""
+    for m in (1e-50, 1e39, float("inf"), float("nan")):
+        with pytest.raises((pn.PnError, ValueError), match="attention_scale"):
+            pn.Rotary(64, attention_scale=m)
+    pn.Rotary(64, attention_scale=1e-30)
