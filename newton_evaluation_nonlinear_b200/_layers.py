@@ -334,7 +334,7 @@ class LinearAttention:
         if isinstance(log_decay, torch.Tensor):
             if log_decay.requires_grad:
                 raise ValueError("log_decay requires a gradient: the decays are fixed, detach it")
-            log_decay = log_decay.cpu().numpy()
+            log_decay = log_decay.to("cpu", torch.float32).numpy()   # (numpy has no bfloat16)
         g = np.ascontiguousarray(log_decay, dtype=np.float32)
         if g.shape != (self.heads,):
             raise ValueError(f"log_decay has shape {g.shape}; ({self.heads},) is wanted")

@@ -91,3 +91,10 @@ def test_attention_scales_beyond_float32_are_refused():
         with pytest.raises((pn.PnError, ValueError), match="attention_scale"):
             pn.Rotary(64, attention_scale=m)
     pn.Rotary(64, attention_scale=1e-30)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32, torch.float64])
+def test_decays_of_any_floating_type(dtype):
+    g = torch.tensor([0.0, -0.5, -2.0], dtype=dtype)
+    att = pn.LinearAttention(3, 1, 8, 8, g)
+    assert np.array_equal(att._args[4], np.array([0.0, -0.5, -2.0], np.float32))
