@@ -338,7 +338,7 @@ class LinearAttention:
         g = np.ascontiguousarray(log_decay, dtype=np.float32)
         if g.shape != (self.heads,):
             raise ValueError(f"log_decay has shape {g.shape}; ({self.heads},) is wanted")
-        self.scale = float(dk) ** -0.5 if scale is None else float(scale)
+        self.scale = max(float(dk), 1.0) ** -0.5 if scale is None else float(scale)   # (a dk below 1 is refused below)
         h = ctypes.c_void_p()
         _ok(lib.pn_linattn_create(ctypes.byref(h), self.heads, self.kv_heads, self.dk, self.dv, _dtypes()[self.dtype],
                                   g.ctypes.data, self.scale))

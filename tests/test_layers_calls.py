@@ -98,3 +98,10 @@ def test_decays_of_any_floating_type(dtype):
     g = torch.tensor([0.0, -0.5, -2.0], dtype=dtype)
     att = pn.LinearAttention(3, 1, 8, 8, g)
     assert np.array_equal(att._args[4], np.array([0.0, -0.5, -2.0], np.float32))
+
+
+@pytest.mark.parametrize("dk", [0, -8])
+def test_widths_below_one_are_refused_as_others_are(dk):
+    """With the default scale too, which dk ** -0.5 would be."""
+    with pytest.raises(pn.PnError, match=f"dk={dk}"):
+        pn.LinearAttention(2, 2, dk, 8, [0.0, 0.0])
