@@ -469,6 +469,11 @@ PN_API void pn_linattn_destroy(pn_linattn h);
  *               is its initial one.  Both 16-byte aligned. */
 PN_API size_t pn_linattn_workspace(pn_linattn h, int backward, int n_seq, long long T, int ragged,
                                    long long max_len);
+/* How a pass is divided (pass 0: forward; 1, 2, 3: dq, dk, dv) where TMA can read its arrays: *columns (64 or
+ * 128) of the states to a CTA of the tcgen05 kernel, 0 where the other one takes it; *parts that sequences are
+ * cut into. */
+PN_API pn_status pn_linattn_split(pn_linattn h, int pass, int n_seq, long long T, int ragged, long long max_len,
+                                  int* columns, int* parts);
 PN_API pn_status pn_linattn_forward(pn_linattn h, int n_seq, long long T, const int* cu_seqlens,
                                     long long max_len, const pn_heads* q, const pn_heads* k,
                                     const pn_heads* v, const float* initial_state, const pn_heads* o,

@@ -97,6 +97,8 @@ SIGNATURES = {
     "pn_linattn_create": (_c_int, [ctypes.POINTER(_vp), _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_float]),
     "pn_linattn_destroy": (None, [_vp]),
     "pn_linattn_workspace": (_c_size, [_vp, _c_int, _c_int, _c_ll, _c_int, _c_ll]),
+    "pn_linattn_split": (_c_int, [_vp, _c_int, _c_int, _c_ll, _c_int, _c_ll, ctypes.POINTER(_c_int),
+                                  ctypes.POINTER(_c_int)]),
     "pn_linattn_forward": (_c_int, [_vp, _c_int, _c_ll, _vp, _c_ll, _heads, _heads, _heads, _vp, _heads, _vp, _vp,
                                     _c_size, _vp]),
     "pn_linattn_backward": (_c_int, [_vp, _c_int, _c_ll, _vp, _c_ll] + [_heads] * 4 + [_vp, _vp] + [_heads] * 3

@@ -271,6 +271,19 @@ size_t pn_linattn_workspace(pn_linattn h, int backward, int n_seq, long long T, 
   return n;
 }
 
+pn_status pn_linattn_split(pn_linattn h, int pass, int n_seq, long long T, int ragged, long long max_len, int* columns, int* parts) {
+  if (!h || !columns || !parts) return seq_fail(PN_ERR_INVALID, "handle, columns or parts is NULL");
+  if (pass < 0 || pass > 3) return seq_fail(PN_ERR_INVALID, "pass=%d: from 0 to 3", pass);
+  Shape s;
+  static const int some = 0;
+  if (pn_status e = check_shape(h, n_seq, T, ragged ? &some : nullptr, max_len, &s)) return e;
+  const int da = pass == 0 || pass == 3 ? h->dk : h->dv, dc = pass == 0 || pass == 3 ? h->dv : h->dk;
+  const bool tc = h->dtype == PN_BF16 && da <= 128 && T > 0;
+  *columns = tc ? tc_columns(h, n_seq, dc) : 0;
+  *parts = tc ? tc_parts(h, n_seq, s.max_len, dc) : mma_parts(h, n_seq, s.max_len, da, dc);
+  return PN_OK;
+}
+
 pn_status pn_linattn_forward(pn_linattn h, int n_seq, long long T, const int* cu_seqlens, long long max_len,
                              const pn_heads* q, const pn_heads* k, const pn_heads* v, const float* initial_state,
                              const pn_heads* o, float* final_state, void* workspace, size_t workspace_bytes,

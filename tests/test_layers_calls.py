@@ -105,3 +105,25 @@ def test_widths_below_one_are_refused_as_others_are(dk):
     """With the default scale too, which dk ** -0.5 would be."""
     with pytest.raises(pn.PnError, match=f"dk={dk}"):
         pn.LinearAttention(2, 2, dk, 8, [0.0, 0.0])
+
+
+def test_split():
+    """Which kernel, how many columns to a CTA, how many parts: the rules at their edges."""
+    import ctypes
+
+    def split(att, pass_, n, T, ragged=0, max_len=0):
+        c, p = ctypes.c_int(-1), ctypes.c_int(-1)
+        assert pn.lib.pn_linattn_split(att.h, pass_, n, T, ragged, max_len, ctypes.byref(c), ctypes.byref(p)) == pn.PN_OK
+        return c.value, p.value
+
+    att = pn.LinearAttention(2, 2, 128, 96, [0.0, 0.0], dtype=torch.bfloat16)
+    assert split(att, 0, 37, 100) == (64, 1) and split(att, 0, 38, 100) == (128, 1)   # 37 x 2 heads x 2 CTAs fit 148 SMs
+    assert split(att, 0, 1, 65536)[1] > 1 and split(att, 0, 1, 65536, 1, 100)[1] == 1
+    wide = pn.LinearAttention(2, 2, 136, 96, [0.0, 0.0], dtype=torch.bfloat16)
+    assert [split(wide, p, 1, 100)[0] for p in range(4)] == [0, 64, 64, 0]
+    assert split(pn.LinearAttention(2, 2, 128, 96, [0.0, 0.0], dtype=torch.float16), 0, 1, 100)[0] == 0
+    c = ctypes.c_int()
+    for args, needle in [((None, 0, 1, 1, 0, 0, c, c), "NULL"), ((att.h, 4, 1, 1, 0, 0, c, c), "pass"),
+                         ((att.h, 0, -1, 1, 0, 0, c, c), "shape"), ((att.h, 0, 1, 1, 0, -1, c, c), "max_len")]:
+        assert pn.lib.pn_linattn_split(*args[:6], *map(ctypes.byref, args[6:])) == pn.PN_ERR_INVALID
+        assert needle in pn.pn_last_error(None)
