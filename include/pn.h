@@ -386,7 +386,10 @@ typedef enum {
   PN_ROT_NTK = 2,     /* base times factor^(rot_dim/(rot_dim - 2)) */
   PN_ROT_YARN = 3     /* f_i (g + (1 - g) / factor), g = clamp((r - beta_slow) / (beta_fast -
                          beta_slow), 0, 1), r = original_length f_i / 2 pi turns over the original
-                         context; m = 0.1 ln(factor) + 1 */
+                         context; m = 0.1 ln(factor) + 1.  This ramp, linear in the turns, is the one
+                         of the method's paper.  A ramp linear in the pair's number, between the (often
+                         rounded) numbers where r is beta_fast and beta_slow, gives other frequencies
+                         between them; models trained with that one do not fit. */
 } pn_rotary_scaling;
 typedef struct {
   int rot_dim;              /* even, 2 .. 256 */
@@ -443,7 +446,9 @@ PN_API pn_status pn_norm_rotary_backward(pn_rotary r, int dtype, int B, int T, i
  * q, k, v and o are of one type (PN_F32, PN_BF16, PN_F16); states are float32, and so are all sums.
  * Prompts of PN_BF16 with dk <= 128 (and gradients, dv too) and rows that TMA can read (16-byte aligned,
  * strides above zero) run on tcgen05: the state before a chunk of 64 rows and the weights between its rows
- * are rounded to bfloat16, once each, for the outputs.  All else runs on the TF32 tensor cores in split form, with float32's
+ * are rounded to bfloat16, once each, for the outputs, whose error in the mean square is 0.0023 of their size (0.0017 is the
+ * rounding of the outputs themselves); states are kept times up to 2^40 either way, so that those below 2^-86 may lose bits
+ * and gradients of final states beyond 2^86 overflow.  All else runs on the TF32 tensor cores in split form, with float32's
  * accuracy.  An infinite or NaN input makes outputs of its sequence and head undefined from up to 63 rows
  * before it (whole chunks are multiplied at once; so do products q.k beyond 2^86); other sequences, padding
  * rows and rows behind the last one never take part. */

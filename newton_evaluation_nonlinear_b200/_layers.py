@@ -205,7 +205,8 @@ class Rotary:
 
     layout    "half" (pair i: elements i and i + rot_dim/2) or "interleaved" (2i and 2i + 1)
     scaling   "none"; "linear" (positions divided by ``factor``); "ntk" (the base stretched by ``factor``); "yarn"
-              (per frequency, by its turns over ``original_length``)
+              (per frequency, by a ramp linear in its turns over ``original_length``, as in the method's paper; models trained
+              with a ramp linear in the pair's number have other frequencies)
     attention_scale   factor on the rotated elements; None: 1, or 0.1 ln(factor) + 1 for "yarn"
 
     The plan holds no device memory; one object serves every device and stream.  Copies, pickled ones too, are plans of
@@ -319,6 +320,11 @@ class LinearAttention:
     log_decay         [heads], finite and <= 0, on the host or a device (read once, here; no gradient is formed for it)
     scale             None: dk ** -0.5
     dtype             of q, k, v and o: torch.float32, bfloat16 or float16; states are float32
+
+    Sums and states are float32.  bfloat16 prompts and gradients of widths up to 128 round the weights between rows and the
+    state before each chunk of 64 rows to bfloat16 for the outputs: these are 0.0023 off in the mean square, where their own
+    rounding makes 0.0017.  An infinite or NaN row makes outputs of its sequence and head undefined from up to 63 rows
+    before it.
 
     Copies, pickled ones too, are handles of their own.
     """

@@ -625,7 +625,8 @@ __global__ void __launch_bounds__(kStepThreads) lin_step_kernel(const __grid_con
     const int r = rg + u * RG;
     s[u] = (on && r < P.dk) ? *reinterpret_cast<const float4*>(S + (long long)r * P.dv) : make_float4(0, 0, 0, 0);
   }
-  // of rows that name one slot the first is computed, the others are padding
+  // Of rows that name one slot the first is computed, the others are padding.  (Each row looks through those before it: 3 % of
+  // 192 rows' time, 10 % of 4096's; at 65535 rows of one head it is what counts.)
   int twice = 0;
   if (P.slots)
     for (int i = tid; i < b; i += kStepThreads) twice |= (P.slots[i] == slot);

@@ -271,3 +271,58 @@ def test_waits_that_give_up_are_reported(dk, dv, n, backward, chunk):
     for s in streams:
         with torch.cuda.stream(s):
             att.check()
+
+
+FIRST_CAPTURED = """
+import torch, newton_evaluation_nonlinear_b200 as pn
+x = [torch.randn(300, 2, 64, device="cuda").to(t) for t in (torch.float32, torch.bfloat16, torch.float16)]
+pos, w = torch.arange(300, device="cuda"), torch.ones(64, device="cuda")
+r = pn.Rotary(64)
+atts = [pn.LinearAttention(2, 2, 64, 64, [-0.1, 0.0], dtype=y.dtype) for y in x]
+states = [torch.zeros(300, 2, 64, 64, device="cuda") for _ in x]
+torch.cuda.synchronize()
+def run():
+    out = []
+    for y, att, s in zip(x, atts, states):
+        s.zero_()
+        out += [*r.apply(y, y, pos), *r.norm_apply(y, y, pos, w, w), *r.norm_backward(y, y, y, y, pos, w, w),
+                *att.forward(y[None], y[None], y[None]), *att.backward(y[None], y[None], y[None], y[None]), att.step(y, y, y, s)]
+    return out
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+print("captured")
+"""
+
+
+def test_first_calls_in_a_capture():
+    """A process whose first calls are captured (no kernel has been loaded before)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
+
+
+def test_lists_beyond_31_bits():
+    """More vectors than 2^30: rows and heads are found by 64-bit divisions."""
+    T, H, K, d = (1 << 24) + 5, 63, 1, 8
+    q, k = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, K, d, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(T, device="cuda")
+    r, w = pn.Rotary(d), torch.ones(d, device="cuda")
+    rows = torch.tensor([0, 1, 77, 1 << 23, (1 << 24) - 1, 1 << 24, T - 1], device="cuda")
+    q[rows], k[rows] = rnd(1, 7, H, d, dtype=torch.bfloat16).cuda(), rnd(2, 7, K, d, dtype=torch.bfloat16).cuda()
+    gq, gk = r.norm_apply(q, k, pos, w, w)
+    wq, wk = r.norm_apply(q[rows], k[rows], rows, w, w)
+    assert torch.equal(gq[rows], wq) and torch.equal(gk[rows], wk)
+    assert int((gq != 0).any(-1).any(-1).sum()) == 7 and int((gk != 0).any(-1).any(-1).sum()) == 7
+    _, _, dwq, dwk = r.norm_backward(q, k, q, k, pos, w, w, out=(gq, gk))
+    dq, dk, wwq, wwk = r.norm_backward(q[rows], k[rows], q[rows], k[rows], rows, w, w)
+    assert torch.equal(gq[rows], dq) and torch.equal(gk[rows], dk)
+    # sums in two orders of 7 x heads terms that are not zero, each 6 sqrt(8) at most: n additions are 2^-24 n of the terms' sum off
+    for a, b, n in ((dwq, wwq, 7 * H), (dwk, wwk, 7 * K)):
+        assert float((a - b).abs().max()) <= 2 * n * 2.0 ** -24 * n * 17
