@@ -1,11 +1,9 @@
 // pn_linattn.cu -- entry points of linear attention with a decay for each head.
 #include <algorithm>
 #include <cmath>
-#include <exception>
-#include <map>
 #include <memory>
 #include <mutex>
-#include <utility>
+#include <vector>
 
 #include "pn_linattn_tc.cuh"
 
@@ -437,9 +435,14 @@ pn_status pn_linattn_debug_waits(pn_linattn h, long long timeout_ns, int stall_c
 }
 
 pn_status pn_linattn_check(void* cuda_stream) {
-  // what each (device, stream) has been told of so far
+  // what each stream has been told of so far
+  struct Told {
+    int dev;
+    void* stream;
+    unsigned count;
+  };
   static std::mutex lock;
-  static std::map<std::pair<int, void*>, unsigned> told;
+  static std::vector<Told> told;
   cudaStream_t st = (cudaStream_t)cuda_stream;
   unsigned count = 0;
   int dev = 0;
@@ -447,14 +450,15 @@ pn_status pn_linattn_check(void* cuda_stream) {
   if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&count, lin_gave_up, sizeof count, 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return seq_fail(PN_ERR_CUDA, "reading the device's count of waits failed: %s", cudaGetErrorString(e));
-  unsigned before;
+  unsigned before = 0;
   try {
     std::lock_guard<std::mutex> g(lock);
-    unsigned& seen = told[{dev, cuda_stream}];
-    before = seen;
+    auto it = std::find_if(told.begin(), told.end(), [&](const Told& t) { return t.dev == dev && t.stream == cuda_stream; });
+    if (it == told.end()) it = told.insert(told.end(), Told{dev, cuda_stream, 0u});
+    before = it->count;
     // (a check of this stream in another thread may have read a later count)
-    if ((int)(count - before) > 0) seen = count;
-  } catch (const std::exception&) {
+    if ((int)(count - before) > 0) it->count = count;
+  } catch (...) {
     return seq_fail(PN_ERR_NOMEM, "out of host memory");
   }
   if ((int)(count - before) > 0)

@@ -246,7 +246,7 @@ def test_waits_that_give_up_are_reported(dk, dv, n, backward, chunk):
         return att.backward(do, q, k, v, initial_state=s0, dstate=s0) if backward else att.forward(q, k, v, initial_state=s0)
 
     want = run()
-    streams = [torch.cuda.Stream() for _ in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.current_stream()]
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
@@ -260,7 +260,7 @@ def test_waits_that_give_up_are_reported(dk, dv, n, backward, chunk):
         run()
     streams[0].synchronize()
     assert pn.lib.pn_linattn_debug_waits(att.h, 2000000000, -1) == pn.PN_OK
-    for s in reversed(streams):   # the other stream's check first: it takes nothing from this one's
+    for s in reversed(streams):   # the other streams' checks first: they take nothing from this one's
         with torch.cuda.stream(s):
             with pytest.raises(pn.PnError) as e:
                 att.check()
