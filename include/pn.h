@@ -444,8 +444,8 @@ PN_API pn_status pn_norm_rotary_backward(pn_rotary r, int dtype, int B, int T, i
  *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T     (dk x dv, float32)
  *   o_t = scale q_t S_t.
  * q, k, v and o are of one type (PN_F32, PN_BF16, PN_F16); states are float32, and so are all sums.
- * Prompts of PN_BF16 with dk <= 128 (and gradients, dv too) and rows that TMA can read (16-byte aligned,
- * strides above zero) run on tcgen05: the state before a chunk of 64 rows and the weights between its rows
+ * Prompts of PN_BF16 with dk <= 128 (and gradients, dv too), 64 rows times heads or more, and rows that TMA can read
+ * (16-byte aligned, strides above zero) run on tcgen05: the state before a chunk of 64 rows and the weights between its rows
  * are rounded to bfloat16, once each, for the outputs, whose error in the mean square is 0.0023 of their size (0.0017 is the
  * rounding of the outputs themselves); states are kept times up to 2^40 either way, so that those below 2^-86 may lose bits
  * and gradients of final states beyond 2^86 overflow.  All else runs on the TF32 tensor cores in split form, with float32's

@@ -321,9 +321,9 @@ class LinearAttention:
     scale             None: dk ** -0.5
     dtype             of q, k, v and o: torch.float32, bfloat16 or float16; states are float32
 
-    Sums and states are float32.  bfloat16 prompts and gradients of widths up to 128 round the weights between rows and the
-    state before each chunk of 64 rows to bfloat16 for the outputs: these are 0.0023 off in the mean square, where their own
-    rounding makes 0.0017.  An infinite or NaN row makes outputs of its sequence and head undefined from up to 63 rows
+    Sums and states are float32.  bfloat16 prompts and gradients of widths up to 128 and 64 rows times heads or more round the
+    weights between rows and the state before each chunk of 64 rows to bfloat16 for the outputs: these are 0.0023 off in the
+    mean square, where their own rounding makes 0.0017.  An infinite or NaN row makes outputs of its sequence and head undefined from up to 63 rows
     before it.
 
     Copies, pickled ones too, are handles of their own.

@@ -45,6 +45,14 @@ int mma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int d
   return (int)std::max(1LL, std::min(want, max_len / (mma_chunk(da) * (2 * ctas <= 148 ? 1 : 4))));
 }
 
+// Whether the tensor-core kernel is for a pass of that many rows (of all sequences) and widths da.  Its rounding of the weights
+// between rows to bfloat16 is one relative error for a whole row, 2^-8 at most: of many rows it averages out (outputs are 1.42
+// times as far off as by their own rounding), of a few it is the outputs' error (up to 2.0 times below 64 rows and heads, 1.46 from
+// there on).  The other kernel then takes 7.5 to 8.4 us in place of 6.8 at width 64, 11 to 12 in place of 8.6 at 128.
+bool tc_takes(const pn_linattn_s* h, long long rows, int da) {
+  return h->dtype == PN_BF16 && da <= 128 && rows > 0 && rows * h->H >= 64;
+}
+
 // Columns of c that one CTA of the tensor-core kernel takes: 64 where 128 leave SMs idle (a and b are then read twice, out of
 // L2, which costs less than a second part).
 int tc_columns(const pn_linattn_s* h, int n_seq, int dc) {
@@ -150,7 +158,7 @@ cudaError_t launch_tc(const LinMaps& maps, const LinPass& P, const LinDecay& G, 
 
 // The tensor-core kernel, where it can take the pass; false where the other one has to.
 bool try_tc(const pn_linattn_s* h, LinPass& P, const LinDecay& G, long long max_len, cudaStream_t st, cudaError_t* e) {
-  if (h->dtype != PN_BF16 || P.da > 128 || P.T < 1) return false;
+  if (!tc_takes(h, P.cu ? P.T : P.n_seq * P.T, P.da)) return false;
   LinMaps maps;
   const int batch = P.cu ? 1 : P.n_seq;
   if (!encode_operand(&maps.a, P.a, P.da, P.H / P.a.per, P.T, batch) ||
@@ -276,7 +284,7 @@ pn_status pn_linattn_split(pn_linattn h, int pass, int n_seq, long long T, int r
   static const int some = 0;
   if (pn_status e = check_shape(h, n_seq, T, ragged ? &some : nullptr, max_len, &s)) return e;
   const int da = pass == 0 || pass == 3 ? h->dk : h->dv, dc = pass == 0 || pass == 3 ? h->dv : h->dk;
-  const bool tc = h->dtype == PN_BF16 && da <= 128 && T > 0;
+  const bool tc = tc_takes(h, s.rows, da);
   *columns = tc ? tc_columns(h, n_seq, dc) : 0;
   *parts = tc ? tc_parts(h, n_seq, s.max_len, dc) : mma_parts(h, n_seq, s.max_len, da, dc);
   return PN_OK;
