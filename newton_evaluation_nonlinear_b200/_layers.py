@@ -76,10 +76,10 @@ def _int(name, n):
 
 def _no_graph(*tensors):
     """Refuses tensors whose gradients torch would expect to be recorded."""
-    import torch
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            import torch
+            if torch.is_grad_enabled():
                 raise ValueError("a tensor requires a gradient, which this call does not record: call it under torch.no_grad() "
                                  "or from a torch.autograd.Function, or detach the tensor")
 
@@ -94,7 +94,7 @@ def _first(name, t):
         B = 1
     else:
         raise ValueError(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    if B > _INT or T > _INT or h > _INT or d > _INT:
+    if t.numel() > _INT and max(t.shape) > _INT:
         raise ValueError(f"{name} is {tuple(t.shape)}: sizes of up to 2^31 - 1 are taken")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -131,21 +131,19 @@ def _output(name, t, like, heads, dim):
     return row
 
 
-def _like(t):
-    """A tensor like t, laid out as it is where that leaves rows contiguous.  (empty_like orders dimensions by their strides;
-    windows that overlap by all but one element have two of one element, and their rows need not come out last.)"""
-    import torch
-    o = torch.empty_like(t)
-    return o if o.stride(-1) == 1 else torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
 def _fresh(t, nd):
-    """The same of a tensor just made."""
+    """(tensor, row as of :func:`_heads`) of one that empty_like has made.  (It orders dimensions by the strides of its model;
+    windows that overlap by all but one element have two of one element, and then the rows need not be contiguous: another
+    tensor takes its place.)"""
     if nd == 4:
-        x, y, z, _ = t.stride()
-        return t.data_ptr(), x, y, z
-    y, z, _ = t.stride()
-    return t.data_ptr(), 0, y, z
+        x, y, z, w = t.stride()
+    else:
+        x = 0
+        y, z, w = t.stride()
+    if w != 1:
+        import torch
+        return _fresh(torch.empty_like(t, memory_format=torch.contiguous_format), nd)
+    return t, (t.data_ptr(), x, y, z)
 
 
 def _rows(*heads):
@@ -247,7 +245,9 @@ class Rotary:
         """(what k and the others are held to, key heads, rows of q and of k, address of positions)."""
         import torch
         like = nd, B, T, H, d, _, device = _first("q", q)
-        K = _int("key heads", k.shape[-2]) if k.dim() == nd else 0
+        K = k.shape[-2] if k.dim() == nd else 0
+        if K > _INT:
+            raise ValueError(f"k is {tuple(k.shape)}: sizes of up to 2^31 - 1 are taken")
         return (like, K, _heads("q", q, like, H, d), _heads("k", k, like, K, d),
                 _ints("positions", positions, (B, T) if nd == 4 else (T,), torch.int64, device))
 
@@ -255,13 +255,15 @@ class Rotary:
     def _out(q, k, like, K, out):
         nd, _, _, H, d, _, _ = like
         if out is None:
-            oq, ok = _like(q), _like(k)
-            return (oq, ok), _fresh(oq, nd), _fresh(ok, nd)
+            import torch
+            (oq, hq), (ok, hk) = _fresh(torch.empty_like(q), nd), _fresh(torch.empty_like(k), nd)
+            return (oq, ok), hq, hk
         oq, ok = out
         return (oq, ok), _output("out[0]", oq, like, H, d), _output("out[1]", ok, like, K, d)
 
     def _rotate(self, q, k, positions, out, inverse):
-        _no_graph(q, k, *(out or ()))
+        if q.requires_grad or k.requires_grad or out is not None:
+            _no_graph(q, k, *(out or ()))
         like, K, hq, hk, pos = self._operands(q, k, positions)
         _, B, T, H, d, _, device = like
         out, oq, ok = self._out(q, k, like, K, out)
@@ -282,7 +284,8 @@ class Rotary:
     def norm_apply(self, q, k, positions, wq, wk, eps: float = 1e-6, out=None):
         """x_j w_j / sqrt(mean(x^2) + eps) of each head vector, then the rotation, in one pass.  The weights are [dim],
         float32 or of the queries' type."""
-        _no_graph(q, k, wq, wk, *(out or ()))
+        if q.requires_grad or k.requires_grad or wq.requires_grad or wk.requires_grad or out is not None:
+            _no_graph(q, k, wq, wk, *(out or ()))
         like, K, hq, hk, pos = self._operands(q, k, positions)
         _, B, T, H, d, _, device = like
         w = _weights(wq, wk, d, device)
@@ -383,8 +386,9 @@ class LinearAttention:
         return (_int("sequences", cu_seqlens.numel() - 1), T, _ints("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, device),
                 int(max_len or 0))
 
-    def _empty(self, q):
-        return _like(q) if self.dv == self.dk else q.new_empty(q.shape[:-1] + (self.dv,))
+    def _empty(self, q, nd):
+        import torch
+        return _fresh(torch.empty_like(q) if self.dv == self.dk else q.new_empty(q.shape[:-1] + (self.dv,)), nd)
 
     def forward(self, q, k, v, initial_state=None, cu_seqlens=None, max_len: Optional[int] = None, out=None):
         """(o, final state) of whole sequences.
@@ -401,8 +405,7 @@ class LinearAttention:
         s0 = _float32("initial_state", initial_state, shape, device)
         state = q.new_empty(shape, dtype=torch.float32) if s0 is None else torch.empty_like(initial_state)
         if out is None:
-            out = self._empty(q)
-            ho = _fresh(out, like[0])
+            out, ho = self._empty(q, like[0])
         else:
             ho = _output("out", out, like, self.heads, self.dv)
         size = lib.pn_linattn_workspace(self.h, 0, n, T, cu is not None, max_len)
@@ -425,9 +428,10 @@ class LinearAttention:
         s0 = _float32("initial_state", initial_state, shape, device)
         ds = _float32("dstate", dstate, shape, device)
         if grads is None:
-            grads = (_like(q), _like(k), _like(v))
-        sizes = ((self.heads, self.dk), (self.kv_heads, self.dk), (self.kv_heads, self.dv))
-        outs = [_output(f"grads[{i}]", g, like, *size) for i, (g, size) in enumerate(zip(grads, sizes))]
+            grads, outs = zip(*[_fresh(torch.empty_like(t), like[0]) for t in (q, k, v)])
+        else:
+            sizes = ((self.heads, self.dk), (self.kv_heads, self.dk), (self.kv_heads, self.dv))
+            outs = [_output(f"grads[{i}]", g, like, *size) for i, (g, size) in enumerate(zip(grads, sizes))]
         ds0 = q.new_empty(shape, dtype=torch.float32)
         size = lib.pn_linattn_workspace(self.h, 1, n, T, cu is not None, max_len)
         keep_w, ws = _workspace(size, q.device)
@@ -460,8 +464,7 @@ class LinearAttention:
         like, hq, hk, hv = self._operands(q, k, v)
         rows, device = like[2], like[-1]
         if out is None:
-            out = self._empty(q)
-            ho = _fresh(out, 3)
+            out, ho = self._empty(q, 3)
         else:
             ho = _output("out", out, like, self.heads, self.dv)
         if states.dim() != 4:
