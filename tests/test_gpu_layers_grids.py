@@ -157,3 +157,34 @@ def test_linear_ragged_parts(dk, dv, K, g, monkeypatch):
         columns, parts = split(dk, dv, 2, K, p, lens)
         assert columns == 64 and parts > 1
     base.run_linear(lens, 2, K, dk, dv, torch.bfloat16, lead=2, tail=5)
+
+
+@pytest.mark.parametrize("n, H, T, d", [(1, 4, 640, 128), (1, 4, 640, 64), (40, 4, 200, 128)])
+def test_linear_bfloat16_rounds_what_it_says(n, H, T, d):
+    """Outputs of the tcgen05 kernel are those of 64-bit chunks in which two things are rounded to bfloat16, once each: the
+    weights between rows and the state before the chunk, both times the powers of the decay that one accumulator for both
+    wants.  What is left are values that float32 and 64 bits round to neighbours: with products and sums up to 2^-17 off and
+    steps of 2^-8 that is one value in 2^8 or fewer, each 2^-7.5 off: 2^-11.5 in the mean square, where a third rounding to
+    bfloat16 would add 2^-9.2 (a half step of 2^-8, uniform, over a uniform mantissa)."""
+    g = torch.tensor([0.0, -1e-3, -0.05, -0.8])[:H]
+    q, k, v = (rnd(i, n, T, H, d, dtype=torch.bfloat16) for i in (1, 2, 3))
+    att = pn.LinearAttention(H, H, d, d, g, dtype=torch.bfloat16)
+    c = ctypes.c_int()
+    assert pn.lib.pn_linattn_split(att.h, 0, n, T, 0, 0, ctypes.byref(c), ctypes.byref(ctypes.c_int())) == pn.PN_OK and c.value > 0
+    o, _ = att.forward(q.cuda(), k.cuda(), v.cuda())
+    C, i = 64, torch.arange(64).double()
+    G = g.double()[:, None]
+    pad = (-T) % C
+    a, b, c = (torch.nn.functional.pad(x[:2].double(), (0, 0, 0, 0, 0, pad)).permute(0, 2, 1, 3) for x in (q, k, v))   # two will do
+    once = lambda x: x.bfloat16().double()  # noqa: E731
+    S, parts = torch.zeros(min(n, 2), H, d, d, dtype=torch.float64), []
+    for r in range(0, T, C):
+        x, y, z = (t[:, :, r:r + C] for t in (a, b, c))
+        P = (x @ y.transpose(-1, -2)).tril() * torch.exp(G * (32 - (i + 1)))[:, None, :]
+        o2 = x @ once(S * torch.exp(G * 32)[:, :, None]) + once(P) @ z
+        parts.append(d ** -0.5 * torch.exp(G * (i + 1 - 32))[..., None] * o2)
+        S = S * torch.exp(G * 64)[:, :, None] + (y * torch.exp(G * (63 - i))[..., None]).transpose(-1, -2) @ z
+    want = torch.cat(parts, 2)[:, :, :T].permute(0, 2, 1, 3)
+    got = o[:2].double().cpu()
+    off = float((got - once(want)).norm() / want.norm())
+    assert off < 2.0 ** -11, off
