@@ -18,11 +18,11 @@
 // too few of them next to sines, weights and sums: each thread copies its pieces of
 // the next vectors to slots of its own in shared memory (cp.async), several vectors
 // ahead, over the borders of tokens too, and needs no barrier to read them.
-// Measured, bfloat16 of width 128: rotation of half of the head, 65536 rows x 20 heads,
-// interleaved, 110 us, 6.1 TB/s, 0.93 of the measured copy rate (183 us with the pieces loaded to
-// registers); norm and rotation of 16384 x 40 heads 65 us, 5.1 TB/s, 0.78 (143 us); its gradient
-// 116 us, 4.3 TB/s, 0.66 (272 us): what is left there is the sums over a group's lanes, the
-// sines and the two products for each value, all in float32.
+// Measured in replayed graphs, bfloat16 of width 128: rotation of half of the head, 65536 rows x 20 heads,
+// interleaved, 107 us, 6.2 TB/s, 0.95 of the measured copy rate (183 us with the pieces loaded to
+// registers); norm and rotation of 16384 x 40 heads 63 us, 5.3 TB/s, 0.82 (143 us); its gradient
+// 110 us, 4.6 TB/s, 0.70 (272 us): what is left there is not the memory but chains of the sums over a group's lanes, the
+// sines and shared-memory reads, at four warps a scheduler.
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
@@ -640,8 +640,8 @@ pn_status run_heads(const pn_rotary_plan* r, int dtype, int B, int T, int Hq, in
     const long long items = rows * (A.blocks[0] + A.blocks[1]);
     // Where instructions bound it (the norm of 16-bit vectors; groups with idle lanes), as many CTAs as run at once, each with a
     // long list, else more and shorter ones, which even out the SMs' shares of the memory: 3 against 16 on an SM, norm of 16384 x
-    // 40 bfloat16 heads of 128 65 and 73 us, rotation of 6135 x 24 float32 heads of 80 21 and 23; rotation of 65536 x 20 bfloat16
-    // heads of 128 128 and 109, norm of 16384 x 20 float32 heads of 128 67 and 61.
+    // 40 bfloat16 heads of 128 63 and 73 us, rotation of 6135 x 24 float32 heads of 80 21 and 23; rotation of 65536 x 20 bfloat16
+    // heads of 128 128 and 107, norm of 16384 x 20 float32 heads of 128 67 and 61.
     const bool busy = ve > 1 && ((norm && es == 2) || A.units < group);
     grid = (int)std::min<long long>((items + per_cta - 1) / per_cta, 148LL * (busy ? 3 : 16));
   }

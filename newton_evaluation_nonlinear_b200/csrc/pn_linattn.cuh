@@ -210,7 +210,7 @@ __device__ __forceinline__ void lin_mma_split(float (&d)[N][4], const LinFrag<4,
 // S is summed in float32 registers (the tensor cores truncate) and copied to
 // shared memory for the outputs.  What it is for is float32, which the tcgen05 kernel
 // does not take: 4 x 16 heads x 4096 rows of width 64 took 616 us by FP32 FMA with
-// 4 x 4 values a thread, which shared memory bounds, and take 338 us so.
+// 4 x 4 values a thread, which shared memory bounds, and take 328 to 338 us so.
 // STATE_ONLY leaves out the outputs: what the part adds to the state, from zero.
 template <typename T, int C, int DA, bool STATE_ONLY>
 __global__ void __launch_bounds__(LinMmaCfg<T, C, DA>::NT, LinMmaCfg<T, C, DA>::CTAS) lin_mma_kernel(const __grid_constant__ LinPass P,

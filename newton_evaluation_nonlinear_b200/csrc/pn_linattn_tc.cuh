@@ -45,9 +45,9 @@
 // two neighbours sit in one thread, and go to shared memory by stmatrix, transposed for the outputs.
 // Loops of several hundred instructions are rolled (unrolled, five roles overran the instruction
 // cache: 3.7 stalls for each instruction issued; 2.1 rolled).
-// Measured, 4 x 37 heads x 4096 rows (one CTA on every SM): width 128 127 us, 4.9 TB/s of the arrays'
-// bytes, 0.74 of the measured copy rate, 0.58 instructions a scheduler and clock, tensor cores
-// busy half of the time; width 64 76 us, 4.1 TB/s.
+// Measured, 4 x 37 heads x 4096 rows (one CTA on every SM): width 128 129 us, 4.8 TB/s of the arrays'
+// bytes, 0.73 of the measured copy rate, 0.58 instructions a scheduler and clock, tensor cores
+// busy half of the time; width 64 69 to 77 us from process to process, 4.0 to 4.5 TB/s.
 #pragma once
 
 #include <type_traits>
