@@ -326,8 +326,8 @@ class LinearAttention:
 
     Sums and states are float32.  bfloat16 prompts and gradients of widths up to 128 and 64 rows times heads or more round the
     weights between rows and the state before each chunk of 64 rows to bfloat16 for the outputs: these are 0.0023 off in the
-    mean square, where their own rounding makes 0.0017.  An infinite or NaN row makes outputs of its sequence and head undefined from up to 63 rows
-    before it.
+    mean square, where their own rounding makes 0.0017.  An infinite or NaN row makes outputs of its sequence and head
+    undefined from up to 63 rows before it.
 
     Copies, pickled ones too, are handles of their own.
     """
@@ -455,8 +455,8 @@ class LinearAttention:
 
         q [rows, heads, dk], k and v with kv_heads.  ``slots``: int64 [rows], the state of each row (None: row b has
         state b); a slot outside the states, or one that an earlier row names, makes its row padding, which is left as it
-        is (in ``out`` too, which overlaps no other argument; without ``out`` such rows are undefined).  ``wq``, ``wk``: the norm of q and k, ``rotary``
-        with ``positions`` (int64 [rows]): their rotation, both in the same pass."""
+        is (in ``out`` too, which overlaps no other argument; without ``out`` such rows are undefined).  ``wq``, ``wk``: the
+        norm of q and k, ``rotary`` with ``positions`` (int64 [rows]): their rotation, both in the same pass."""
         import torch
         _no_graph(q, k, v, states, wq, wk, out)
         if q.dim() != 3:
