@@ -47,8 +47,8 @@ int mma_parts(const pn_linattn_s* h, int n_seq, long long max_len, int da, int d
 
 // Whether the tensor-core kernel is for a pass of that many rows (of all sequences) and widths da.  Its rounding of the weights
 // between rows to bfloat16 is one relative error for a whole row, 2^-8 at most: of many rows it averages out (outputs are 1.42
-// times as far off as by their own rounding), of a few it is the outputs' error (up to 2.0 times below 64 rows and heads, 1.46 from
-// there on).  The other kernel then takes 7.5 to 8.4 us in place of 6.8 at width 64, 11 to 12 in place of 8.6 at 128.
+// times as far off as by their own rounding), of a few it is the outputs' error (up to 2.0 times below 64 rows and heads, 1.53 from
+// there on, in thousands of drawn calls).  The other kernel then takes 7.5 to 8.4 us in place of 6.8 at width 64, 11 to 12 in place of 8.6 at 128.
 bool tc_takes(const pn_linattn_s* h, long long rows, int da) {
   return h->dtype == PN_BF16 && da <= 128 && rows > 0 && rows * h->H >= 64;
 }
